@@ -27,8 +27,11 @@ LAYOUT_AUTO, LAYOUT_SPREAD, LAYOUT_ONE_XCD = 0, 1, 2
 RECURRENCE_AUTO, RECURRENCE_ALL_TO_ALL, RECURRENCE_LOOKAHEAD = 0, 1, 2
 KERNEL_NAMES = {K_GATHER: "gather", K_GRAM: "gram", K_CHAIN: "chain", K_PIPE: "pipe", K_TRAIN: "train"}
 
+MX4, MX8 = 0, 1
+
 LOSS_IDS = {"logistic": LOGISTIC, "squared": SQUARED, "poisson": POISSON}
 STORAGE_IDS = {"bf16": BF16, "fp32": FP32, "fp16": FP16, "fp8": FP8}
+MX_FORMATS = {"mx4": MX4, "mx8": MX8}
 
 # every entry point declared in include/casgd.h: name -> (restype, argtypes)
 _VP, _I64, _U64, _I, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_uint64, ctypes.c_int, ctypes.c_float
@@ -55,6 +58,18 @@ SIGNATURES = {
     "casgd_peak_copy": (_I, [_VP, _VP, _I64, _VP]),
     "casgd_peak_mfma": (_I, [_VP, _I, _I, _VP]),
     "casgd_peak_read": (_I, [_VP, _I64, _VP, _I, _VP]),
+    "casgd_mx_ld": (_I64, [_I64]),
+    "casgd_mx_quantize": (_I, [_VP, _I, _I64, _I64, _I64, _I, _VP, _VP, _VP]),
+    "casgd_mx_dequantize": (_I, [_VP, _VP, _I, _I64, _I64, _VP, _I, _I64, _VP]),
+    "casgd_mx4_linear_workspace": (_I64, [_I64, _I64, _I64]),
+    "casgd_mx4_linear": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _VP, _I64, _VP, _I, _I64, _VP, _I64, _VP]),
+    "casgd_mx4_grad_input": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _VP, _I64, _VP, _I, _I64, _VP]),
+    "casgd_mx8_grad_weight": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _VP, _I64, _VP, _I, _I64, _I, _VP]),
+    "casgd_token_logps": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _VP, _VP]),
+    "casgd_pref_workspace": (_I64, [_I64]),
+    "casgd_pref_loss": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _VP, _I64, _VP, _I, _F, _F, _I, _VP, _VP, _VP, _VP, _VP,
+                             _VP, _I64, _VP]),
+    "casgd_pref_grad": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _VP, _I64, _VP, _VP, _VP, _VP, _I64, _VP]),
 }
 
 _lib = None
@@ -278,4 +293,247 @@ def unpack_gram(G_packed: np.ndarray, s: int, b: int) -> dict:
         rowblk = G_packed[base:base + b * j * b].reshape(b, j * b)
         for t in range(j):
             out[(j, t)] = rowblk[:, t * b:(t + 1) * b]
+    return out
+
+
+# -- operators of a low-precision linear layer and its preference loss
+
+_TYPES = {}  # torch dtype -> element type id
+
+
+def _type_id(dtype, name):
+    if not _TYPES:
+        import torch
+        _TYPES.update({torch.bfloat16: BF16, torch.float32: FP32, torch.float16: FP16})
+    t = _TYPES.get(dtype)
+    if t is None:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32, not {dtype}")
+    return t
+
+
+def _rows_of(t, name):
+    """(element type, rows, columns, row stride) of a GPU matrix whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    rows, cols = t.shape
+    stride, step = t.stride()
+    if cols < 1:
+        raise ValueError(f"{name} must have at least one column")
+    if (step != 1 and cols > 1) or (stride < cols and rows > 1):
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return _type_id(t.dtype, name), rows, cols, max(stride, cols)
+
+
+def _vector(t, dtype, count, name, device):
+    if t.device != device or t.dtype != dtype or not t.is_contiguous() or t.numel() != count:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {count} elements on {device}")
+    return t.data_ptr()
+
+
+def _call(device, entry, *args):
+    """Call an entry point on torch's current stream of the tensors' device."""
+    import torch
+    fn = getattr(_lib or load(), entry)
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+    if rc != OK:
+        _check(rc, entry)
+
+
+def mx_ld(cols: int) -> int:
+    """Padded row length of a microscaled matrix."""
+    return (cols + 127) // 128 * 128
+
+
+class MXMatrix:
+    """A rows x cols matrix in a microscaled format (see include/casgd.h).
+
+    fmt: "mx4" or "mx8"; codes uint8 [rows, ld / 2] or [rows, ld], scales
+    uint8 [rows, ld / 32], ld = mx_ld(cols); both contiguous on one GPU.
+    """
+
+    __slots__ = ("fmt", "codes", "scales", "rows", "cols")
+
+    def __init__(self, fmt: str, codes, scales, cols: int):
+        import torch
+        if fmt not in MX_FORMATS:
+            raise ValueError(f"fmt must be one of {sorted(MX_FORMATS)}")
+        if cols < 1:
+            raise ValueError("cols must be at least 1")
+        ld = mx_ld(cols)
+        rows = codes.shape[0]
+        if tuple(codes.shape) != (rows, ld // 2 if fmt == "mx4" else ld) or tuple(scales.shape) != (rows, ld // 32):
+            raise ValueError(f"codes and scales do not fit rows of {cols} elements in {fmt}")
+        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+            raise ValueError("codes and scales must be uint8")
+        if not (codes.is_cuda and codes.device == scales.device):
+            raise ValueError("codes and scales must be on one GPU")
+        if not (codes.is_contiguous() and scales.is_contiguous()):
+            raise ValueError("codes and scales must be contiguous")
+        self.fmt, self.codes, self.scales, self.rows, self.cols = fmt, codes, scales, rows, int(cols)
+
+    def _need(self, fmt, name, device):
+        if self.fmt != fmt:
+            raise ValueError(f"{name} must be in {fmt}")
+        if self.codes.device != device:
+            raise ValueError(f"{name} must be on {device}")
+
+
+def mx_quantize(x, fmt: str) -> MXMatrix:
+    """x (a GPU matrix of bf16, fp16 or float32) in a microscaled format."""
+    import torch
+    ty, rows, cols, stride = _rows_of(x, "x")
+    if fmt not in MX_FORMATS:
+        raise ValueError(f"fmt must be one of {sorted(MX_FORMATS)}")
+    ld = mx_ld(cols)
+    codes = torch.empty((rows, ld // 2 if fmt == "mx4" else ld), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((rows, ld // 32), dtype=torch.uint8, device=x.device)
+    _call(x.device, "casgd_mx_quantize", x.data_ptr(), ty, rows, cols, stride, MX_FORMATS[fmt], codes.data_ptr(),
+          scales.data_ptr())
+    return MXMatrix(fmt, codes, scales, cols)
+
+
+def mx_dequantize(q: MXMatrix, dtype):
+    """The values of a microscaled matrix, rounded to dtype."""
+    import torch
+    ty = _type_id(dtype, "dtype")
+    device = q.codes.device
+    out = torch.empty((q.rows, q.cols), dtype=dtype, device=device)
+    _call(device, "casgd_mx_dequantize", q.codes.data_ptr(), q.scales.data_ptr(), MX_FORMATS[q.fmt], q.rows, q.cols,
+          out.data_ptr(), ty, q.cols)
+    return out
+
+
+def mx4_linear(x, w: MXMatrix, out_dtype=None):
+    """y = Q4(x) W^T for x [m, k] and W [n, k] kept in mx4; y of out_dtype (x's by default)."""
+    import torch
+    ty, m, k, stride = _rows_of(x, "x")
+    device = x.device
+    w._need("mx4", "w", device)
+    if w.cols != k:
+        raise ValueError(f"x has {k} columns and w {w.cols}")
+    out_dtype = out_dtype or x.dtype
+    out_ty = _type_id(out_dtype, "out_dtype")
+    y = torch.empty((m, w.rows), dtype=out_dtype, device=device)
+    if y.numel() == 0:
+        return y
+    need = load().casgd_mx4_linear_workspace(m, k, w.rows)
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    _call(device, "casgd_mx4_linear", x.data_ptr(), ty, m, k, stride, w.codes.data_ptr(), w.scales.data_ptr(), w.rows,
+          y.data_ptr(), out_ty, w.rows, ws.data_ptr(), need)
+    return y
+
+
+def mx4_grad_input(dy, w: MXMatrix, out_dtype=None):
+    """dx = dy W for dy [m, n] and W [n, k] kept in mx4; dx of out_dtype (dy's by default)."""
+    import torch
+    ty, m, n, stride = _rows_of(dy, "dy")
+    device = dy.device
+    w._need("mx4", "w", device)
+    if w.rows != n:
+        raise ValueError(f"dy has {n} columns and w {w.rows} rows")
+    out_dtype = out_dtype or dy.dtype
+    out_ty = _type_id(out_dtype, "out_dtype")
+    dx = torch.empty((m, w.cols), dtype=out_dtype, device=device)
+    _call(device, "casgd_mx4_grad_input", dy.data_ptr(), ty, m, n, stride, w.codes.data_ptr(), w.scales.data_ptr(),
+          w.cols, dx.data_ptr(), out_ty, w.cols)
+    return dx
+
+
+def mx8_grad_weight(dy, x: MXMatrix, out=None, accumulate: bool = False, out_dtype=None):
+    """dW = dy^T X for dy [t, n] and the activations X [t, k] checkpointed in mx8.
+
+    out: the [n, k] result (float32 unless out_dtype says otherwise);
+    accumulate adds to it.
+    """
+    import torch
+    ty, t, n, stride = _rows_of(dy, "dy")
+    device = dy.device
+    x._need("mx8", "x", device)
+    if x.rows != t:
+        raise ValueError(f"dy has {t} rows and x {x.rows}")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty((n, x.cols), dtype=out_dtype or torch.float32, device=device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError("out and out_dtype disagree")
+    out_ty, rows, cols, out_stride = _rows_of(out, "out")
+    if (rows, cols) != (n, x.cols) or out.device != device:
+        raise ValueError(f"out must be {n} x {x.cols} on {device}")
+    _call(device, "casgd_mx8_grad_weight", dy.data_ptr(), ty, t, n, stride, x.codes.data_ptr(), x.scales.data_ptr(),
+          x.cols, out.data_ptr(), out_ty, out_stride, 1 if accumulate else 0)
+    return out
+
+
+def token_logps(logits, labels):
+    """Log probability of each row's label (int64; negative: masked, 0)."""
+    import torch
+    ty, t, v, stride = _rows_of(logits, "logits")
+    device = logits.device
+    pl = _vector(labels, torch.int64, t, "labels", device)
+    logps = torch.empty(t, dtype=torch.float32, device=device)
+    _call(device, "casgd_token_logps", logits.data_ptr(), ty, t, v, stride, pl, logps.data_ptr())
+    return logps
+
+
+class PrefLoss:
+    """What pref_loss returns: loss and margin per pair, logps per token, and what pref_grad needs."""
+
+    __slots__ = ("loss", "margin", "logps", "stats", "slope", "logits", "labels", "offsets", "pairs")
+
+
+def pref_loss(logits, labels, offsets, ref_logps=None, beta: float = 0.1, loss: str = "logistic",
+              smoothing: float = 0.0, average: bool = False) -> PrefLoss:
+    """Preference loss of paired log ratios (see casgd_pref_loss).
+
+    logits [tokens, vocab]; labels int64 [tokens], negative where masked;
+    offsets int64 [2 pairs + 1] on the GPU: chosen and rejected sequences in
+    turn; ref_logps float32 [tokens] or None; loss "logistic" or "squared".
+    The result keeps references to logits, labels and offsets for pref_grad.
+    """
+    import torch
+    if loss not in ("logistic", "squared"):
+        raise ValueError("loss must be logistic or squared")
+    ty, t, v, stride = _rows_of(logits, "logits")
+    device = logits.device
+    pl = _vector(labels, torch.int64, t, "labels", device)
+    count = offsets.numel()
+    if count < 3 or count % 2 == 0:
+        raise ValueError("offsets must hold 2 pairs + 1 entries")
+    po = _vector(offsets, torch.int64, count, "offsets", device)
+    pr = None if ref_logps is None else _vector(ref_logps, torch.float32, t, "ref_logps", device)
+    r = PrefLoss()
+    r.pairs, r.logits, r.labels, r.offsets = count // 2, logits, labels, offsets
+    r.loss = torch.empty(r.pairs, dtype=torch.float32, device=device)
+    r.margin = torch.empty(r.pairs, dtype=torch.float32, device=device)
+    r.slope = torch.empty(2 * r.pairs, dtype=torch.float32, device=device)
+    r.logps = torch.empty(t, dtype=torch.float32, device=device)
+    r.stats = torch.empty((t, 2), dtype=torch.float32, device=device)
+    ws = torch.empty(t, dtype=torch.float64, device=device)
+    _call(device, "casgd_pref_loss", logits.data_ptr(), ty, t, v, stride, pl, po, r.pairs, pr, LOSS_IDS[loss], beta,
+          smoothing, 1 if average else 0, r.loss.data_ptr(), r.margin.data_ptr(), r.logps.data_ptr(),
+          r.stats.data_ptr(), r.slope.data_ptr(), ws.data_ptr(), 8 * t)
+    return r
+
+
+def pref_grad(fwd: PrefLoss, grad_loss, out=None):
+    """Gradient of sum(grad_loss * loss) in the logits; out may be fwd.logits itself."""
+    import torch
+    logits = fwd.logits
+    ty, t, v, stride = _rows_of(logits, "logits")
+    device = logits.device
+    pg = _vector(grad_loss, torch.float32, fwd.pairs, "grad_loss", device)
+    if out is None:
+        out = torch.empty((t, v), dtype=logits.dtype, device=device)
+    out_ty, rows, cols, out_stride = _rows_of(out, "out")
+    if (out_ty, rows, cols) != (ty, t, v) or out.device != device:
+        raise ValueError(f"out must be {t} x {v} of {logits.dtype} on {device}")
+    _call(device, "casgd_pref_grad", logits.data_ptr(), ty, t, v, stride, fwd.labels.data_ptr(),
+          fwd.offsets.data_ptr(), fwd.pairs, fwd.stats.data_ptr(), fwd.slope.data_ptr(), pg, out.data_ptr(), out_stride)
     return out

@@ -646,6 +646,12 @@ int run_train_pipe(casgd_ctx* h, int s, int b, float eta, uint64_t base_seed, ui
 
 }  // namespace
 
+// the operators' entry points in the other sources report through these
+namespace casgd {
+int api_fail(int code, const char* msg) { return fail(code, msg); }
+int api_hip_fail(hipError_t e, const char* what) { return hip_fail(e, what); }
+}  // namespace casgd
+
 extern "C" {
 
 const char* casgd_last_error(void) { return g_last_error.c_str(); }

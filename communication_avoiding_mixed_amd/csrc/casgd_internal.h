@@ -224,4 +224,38 @@ hipError_t launch_peak_mfma(float* out, int workgroups, int iters, hipStream_t s
 // with direct-to-LDS loads; out[workgroups * 8] receives ring words.
 hipError_t launch_peak_read(const void* src, int64_t bytes, float* out, int workgroups, hipStream_t stream);
 
+// Set the calling thread's last error and return the code (casgd_api.hip);
+// api_hip_fail appends the runtime's text.
+int api_fail(int code, const char* msg);
+int api_hip_fail(hipError_t e, const char* what);
+
+// Operators of a low-precision linear layer.  Element types are enum
+// casgd_storage without fp8, formats enum casgd_mx_format.
+namespace mx {
+
+constexpr int64_t kMaxDim = 0x7FFFFF00;  // rows and columns
+
+// Why a call's arguments are refused, or nullptr.
+inline const char* bad_matrix(int64_t rows, int64_t cols, int64_t stride, int type) {
+  if (type != kStoreBF16 && type != kStoreF32 && type != kStoreF16) return "element type must be bf16, fp32 or fp16";
+  if (rows < 0 || rows > kMaxDim) return "rows out of range";
+  if (cols < 1 || cols > kMaxDim) return "columns out of range";
+  if (rows > 1 && stride < cols) return "row stride shorter than a row";
+  return nullptr;
+}
+inline const char* bad_codes(const uint8_t* codes, const uint8_t* scales, int64_t rows, int format) {
+  if (format != 0 && format != 1) return "unknown microscaled format";
+  if (rows > 0 && (!codes || !scales)) return "NULL codes or scales";
+  if (reinterpret_cast<uintptr_t>(codes) % 16 != 0) return "codes must be 16-byte aligned";
+  if (reinterpret_cast<uintptr_t>(scales) % 4 != 0) return "scales must be 4-byte aligned";
+  return nullptr;
+}
+
+hipError_t launch_quantize(int format, int type, const void* x, int64_t rows, int64_t cols, int64_t stride, uint8_t* codes,
+                           uint8_t* scales, hipStream_t stream);
+hipError_t launch_dequantize(int format, int type, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                             void* out, int64_t stride, hipStream_t stream);
+
+}  // namespace mx
+
 }  // namespace casgd

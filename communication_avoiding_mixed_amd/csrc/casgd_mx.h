@@ -1,0 +1,239 @@
+// Device helpers shared by the operators of a low-precision linear layer and
+// its preference loss: 8-element loads and stores of bf16, fp16 and float32
+// rows, and the microscaled formats.
+//
+// A microscaled row is cut into blocks of 32 elements.  A block has one scale
+// 2^(byte - 127) and elements of E2M1 (MX4: 0, .5, 1, 1.5, 2, 3, 4, 6 and
+// their negatives) or OCP E4M3 (MX8, up to 448).  byte is the least one for
+// which max|x| / scale is at most the largest element, so no element
+// saturates; it is at least 1, so a scale is never a float32 subnormal.  A
+// block that holds a NaN or an infinity has byte 255 and zero elements: it
+// stands for NaN, and 2^(255 - 127) as float bits is an infinity, whose
+// product with the zero elements is the NaN.
+#pragma once
+
+#include "casgd_device.h"
+
+namespace casgd {
+namespace mx {
+
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+// rows may start at any element: vector accesses are declared with the
+// alignment of one element (global memory takes any alignment here)
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(1)));
+
+constexpr int kBF16 = 0, kF32 = 1, kF16 = 2;  // enum casgd_storage
+constexpr int kMx4 = 0, kMx8 = 1;             // enum casgd_mx_format
+constexpr int kBlock = 32;
+constexpr int kLdMultiple = 128;
+
+__host__ __device__ __forceinline__ int64_t ld_of(int64_t cols) {
+  return (cols + kLdMultiple - 1) / kLdMultiple * kLdMultiple;
+}
+
+template <int TY>
+struct Elem {
+  using type = uint16_t;
+};
+template <>
+struct Elem<kF32> {
+  using type = float;
+};
+
+template <int TY>
+__device__ __forceinline__ float load1(const typename Elem<TY>::type* p) {
+  if constexpr (TY == kF32)
+    return *p;
+  else if constexpr (TY == kBF16)
+    return bf16_to_f32(*p);
+  else
+    return f16_to_f32_hw(*p);
+}
+
+template <int TY>
+__device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b) {
+  if constexpr (TY == kBF16) {
+    a = __uint_as_float(w << 16);
+    b = __uint_as_float(w & 0xFFFF0000u);
+  } else {
+    a = f16_to_f32_hw(w & 0xFFFFu);
+    b = f16_to_f32_hw(w >> 16);
+  }
+}
+
+// 8 consecutive elements as stored: 16 bytes, or 32 of float32
+template <int TY>
+struct Raw8 {
+  u32x4 w[TY == kF32 ? 2 : 1];
+};
+
+template <int TY>
+__device__ __forceinline__ Raw8<TY> load_raw8(const typename Elem<TY>::type* p) {
+  Raw8<TY> r;
+  r.w[0] = *reinterpret_cast<const u32x4_any*>(p);
+  if constexpr (TY == kF32) r.w[1] = *reinterpret_cast<const u32x4_any*>(p + 4);
+  return r;
+}
+
+template <int TY>
+__device__ __forceinline__ void widen8(const Raw8<TY>& r, float v[8]) {
+  if constexpr (TY == kF32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = __uint_as_float(r.w[0][i]);
+      v[4 + i] = __uint_as_float(r.w[1][i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpack2<TY>(r.w[0][i], v[2 * i], v[2 * i + 1]);
+  }
+}
+
+// 8 elements from column c of a row of `cols`; zeros past its end
+template <int TY>
+__device__ __forceinline__ void load8(const typename Elem<TY>::type* row, int64_t c, int64_t cols, float v[8]) {
+  if (c + 8 <= cols) {
+    widen8<TY>(load_raw8<TY>(row + c), v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? load1<TY>(row + c + i) : 0.f;
+  }
+}
+
+typedef __bf16 bf16x2_hw __attribute__((ext_vector_type(2)));
+typedef float f32x2_hw __attribute__((ext_vector_type(2)));
+
+// One float32 as bits of the output type: a single rounding to nearest even
+// (float32: none), by the hardware conversions.
+template <int TY>
+__device__ __forceinline__ uint16_t narrow1(float v) {
+  if constexpr (TY == kBF16)
+    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+  else
+    return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+}
+
+template <int TY>
+__device__ __forceinline__ uint32_t narrow2(float a, float b) {
+  return static_cast<uint32_t>(narrow1<TY>(a)) | (static_cast<uint32_t>(narrow1<TY>(b)) << 16);
+}
+
+template <int TY>
+__device__ __forceinline__ void store1(typename Elem<TY>::type* p, float v) {
+  if constexpr (TY == kF32)
+    *p = v;
+  else
+    *p = narrow1<TY>(v);
+}
+
+template <int TY>
+__device__ __forceinline__ void store8(typename Elem<TY>::type* row, int64_t c, int64_t cols, const float v[8]) {
+  if (c + 8 <= cols) {
+    if constexpr (TY == kF32) {
+      u32x4 a, b;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i] = __float_as_uint(v[i]);
+        b[i] = __float_as_uint(v[4 + i]);
+      }
+      *reinterpret_cast<u32x4_any*>(row + c) = a;
+      *reinterpret_cast<u32x4_any*>(row + c + 4) = b;
+    } else {
+      u32x4 a;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = narrow2<TY>(v[2 * i], v[2 * i + 1]);
+      *reinterpret_cast<u32x4_any*>(row + c) = a;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < cols) store1<TY>(row + c + i, v[i]);
+  }
+}
+
+// Scale byte of a block from the bits of its max |x|.  With amax = m 2^e,
+// 1 <= m < 2, the scale is 2^(e - 2) (largest 6 = 1.5 * 2^2) or 2^(e - 8)
+// (448 = 1.75 * 2^8), one binade more where m exceeds 1.5 or 1.75: adding
+// the complement of that fraction carries into the exponent exactly then.
+template <int FMT>
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
+  if (amax >= 0x7F800000u) return 255u;
+  constexpr uint32_t carry = FMT == kMx4 ? 0x3FFFFFu : 0x1FFFFFu;
+  constexpr int top = FMT == kMx4 ? 2 : 8;
+  const int e = static_cast<int>((amax + carry) >> 23) - top;
+  return static_cast<uint32_t>(e < 1 ? 1 : e);
+}
+
+__device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// 8 elements / scale as E2M1 codes, element i in bits 4i .. 4i + 3 (nearest
+// even, the hardware conversion; nothing saturates by the choice of scale)
+__device__ __forceinline__ uint32_t encode_mx4(const float v[8], uint32_t byte) {
+  if (byte == 255u) return 0u;
+  const float s = scale_value(byte);
+  uint32_t r = 0;
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[0], v[1], s, 0);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[2], v[3], s, 1);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[4], v[5], s, 2);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[6], v[7], s, 3);
+  return r;
+}
+
+// 8 elements / scale as E4M3 codes.  The reciprocal of a power of two is
+// exact: 2^(127 - byte), bits (254 - byte) << 23, byte <= 247 here.
+__device__ __forceinline__ u32x2 encode_mx8(const float v[8], uint32_t byte) {
+  if (byte == 255u) return u32x2{0u, 0u};
+  const float inv = scale_value(254u - byte);
+  u32x2 r;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    int w = 0;
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h] * inv, v[4 * h + 1] * inv, w, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h + 2] * inv, v[4 * h + 3] * inv, w, true);
+    r[h] = static_cast<uint32_t>(w);
+  }
+  return r;
+}
+
+// the values of 8 codes; exact (the scale is a power of two)
+__device__ __forceinline__ void decode_mx4(uint32_t w, float scale, float v[8]) {
+  f32x2_hw p;
+  p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
+  v[0] = p.x * scale, v[1] = p.y * scale;
+  p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
+  v[2] = p.x * scale, v[3] = p.y * scale;
+  p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
+  v[4] = p.x * scale, v[5] = p.y * scale;
+  p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
+  v[6] = p.x * scale, v[7] = p.y * scale;
+}
+
+__device__ __forceinline__ void decode_mx8(u32x2 w, float scale, float v[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const f32x2_hw a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w[h]), false);
+    const f32x2_hw b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w[h]), true);
+    v[4 * h] = a.x * scale, v[4 * h + 1] = a.y * scale;
+    v[4 * h + 2] = b.x * scale, v[4 * h + 3] = b.y * scale;
+  }
+}
+
+__device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// max over aligned groups of 4 lanes (one block of 32 elements)
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  v = max_u32(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0xB1, 0xF, 0xF, false)));
+  v = max_u32(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x4E, 0xF, 0xF, false)));
+  return v;
+}
+
+__device__ __forceinline__ uint32_t amax_bits(const float v[8]) {
+  uint32_t a = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = max_u32(a, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  return a;
+}
+
+}  // namespace mx
+}  // namespace casgd

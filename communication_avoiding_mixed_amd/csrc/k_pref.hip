@@ -1,0 +1,299 @@
+// Preference loss of paired log ratios and its gradient in the logits.
+//
+//   lp_t  = z_t[y_t] - log sum_v exp z_t[v]      (tokens with y_t >= 0)
+//   h     = sum_{chosen} (lp_t - ref_t) - sum_{rejected} (lp_t - ref_t)
+//   logistic  l = (1 - eps) log(1 + exp(-beta h)) + eps log(1 + exp(beta h))
+//   squared   l = (h - 1 / (2 beta))^2
+//   dz_t[v] = g l'(h) (+-1) (1[v = y_t] - exp(z_t[v] - lse_t))
+//
+// Three launches: a row kernel (running max and sum of each row's softmax),
+// a pair kernel (float64 sums of the pair's tokens in a fixed order) and the
+// gradient's row kernel.  The rows are read twice and written once, since a
+// pair's slope needs all of its rows; both row kernels are bound by that
+// traffic.
+#include "casgd.h"
+#include "casgd_internal.h"
+#include "casgd_mx.h"
+
+namespace casgd {
+namespace mx {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+
+// A running (max, sum of exp(z - max)).  A max of -inf (nothing seen, or only
+// -inf) leaves the sum at 0, so no inf - inf is formed.
+struct MaxSum {
+  float m, s;
+};
+__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b) {
+  const float m = fmaxf(a.m, b.m);
+  if (m == -INFINITY) return {m, a.s + b.s};
+  return {m, a.s * exp_hw(a.m - m) + b.s * exp_hw(b.m - m)};
+}
+
+// One workgroup per row.  NaN: v_max drops NaN operands, but exp(NaN - m) in
+// the sum keeps it.
+template <int TY>
+__global__ __launch_bounds__(kThreads) void row_stats_kernel(const typename Elem<TY>::type* __restrict__ logits, int64_t vocab,
+                                                            int64_t stride, const int64_t* __restrict__ labels,
+                                                            float* __restrict__ logps, double* __restrict__ logps64,
+                                                            float2* __restrict__ stats) {
+  __shared__ MaxSum part[kWaves];
+  const int64_t t = blockIdx.x;
+  const int64_t label = labels[t];
+  if (label < 0) {
+    if (threadIdx.x == 0) {
+      logps[t] = 0.f;
+      if (logps64) logps64[t] = 0.0;
+      if (stats) stats[t] = make_float2(0.f, 1.f);
+    }
+    return;
+  }
+  const auto* row = logits + t * stride;
+  MaxSum acc = {-INFINITY, 0.f};
+  for (int64_t c = static_cast<int64_t>(threadIdx.x) * 8; c < vocab; c += kThreads * 8) {
+    float v[8];
+    if (c + 8 <= vocab) {
+      widen8<TY>(load_raw8<TY>(row + c), v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = c + i < vocab ? load1<TY>(row + c + i) : -INFINITY;
+    }
+    float m = acc.m;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, v[i]);
+    const float base = m == -INFINITY ? 0.f : m;
+    float s = acc.s * exp_hw(acc.m - base);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += exp_hw(v[i] - base);
+    acc = {m, s};
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) acc = join(acc, MaxSum{__shfl_xor(acc.m, o, 64), __shfl_xor(acc.s, o, 64)});
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = acc;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  acc = part[0];
+  for (int w = 1; w < kWaves; ++w) acc = join(acc, part[w]);
+  // a label past the vocabulary is not read: its row becomes NaN
+  const float z = label < vocab ? load1<TY>(row + label) : NAN;
+  const double lp = (static_cast<double>(z) - acc.m) - log(static_cast<double>(acc.s));
+  logps[t] = static_cast<float>(lp);
+  if (logps64) logps64[t] = lp;
+  if (stats) stats[t] = make_float2(acc.m, 1.f / acc.s);
+}
+
+__device__ __forceinline__ int64_t clamp_row(int64_t r, int64_t tokens) { return r < 0 ? 0 : r > tokens ? tokens : r; }
+
+// One workgroup per pair: each lane sums its tokens in float64, then lanes
+// and waves join in a fixed order.
+__global__ __launch_bounds__(kThreads) void pair_kernel(const double* __restrict__ logps64, const float* __restrict__ ref,
+                                                       const int64_t* __restrict__ labels, const int64_t* __restrict__ offsets,
+                                                       int64_t tokens, int kind, float beta, float smoothing, int average,
+                                                       float* __restrict__ loss, float* __restrict__ margin,
+                                                       float* __restrict__ slope) {
+  __shared__ double sums[2][kWaves], counts[2][kWaves];
+  const int64_t p = blockIdx.x;
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    const int64_t a = clamp_row(offsets[2 * p + side], tokens), b = clamp_row(offsets[2 * p + side + 1], tokens);
+    double s = 0.0, n = 0.0;
+    for (int64_t t = a + threadIdx.x; t < b; t += kThreads)
+      if (labels[t] >= 0) {
+        s += logps64[t] - (ref ? static_cast<double>(ref[t]) : 0.0);
+        n += 1.0;
+      }
+    s = group_sum_d<64>(s);
+    n = group_sum_d<64>(n);
+    if ((threadIdx.x & 63) == 0) {
+      sums[side][threadIdx.x >> 6] = s;
+      counts[side][threadIdx.x >> 6] = n;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  double mean[2], per[2];
+  for (int side = 0; side < 2; ++side) {
+    double s = 0.0, n = 0.0;
+    for (int w = 0; w < kWaves; ++w) {
+      s += sums[side][w];
+      n += counts[side][w];
+    }
+    per[side] = average && n > 1.0 ? 1.0 / n : 1.0;
+    mean[side] = s * per[side];
+  }
+  const double h = mean[0] - mean[1], bt = beta, eps = smoothing;
+  double l, d;
+  if (kind == kLogistic) {
+    const double u = bt * h;
+    const double e = exp(-fabs(u));
+    const double sig_neg = u >= 0.0 ? e / (1.0 + e) : 1.0 / (1.0 + e);  // logistic function of -u
+    // a term of weight zero is left out, so that an infinite u keeps a finite loss
+    l = (1.0 - eps) * loss_value<kLogistic>(u, 1.0) + (eps > 0.0 ? eps * loss_value<kLogistic>(u, -1.0) : 0.0);
+    d = bt * (eps - sig_neg);
+  } else {
+    const double r = h - 0.5 / bt;
+    l = r * r;
+    d = 2.0 * r;
+  }
+  loss[p] = static_cast<float>(l);
+  margin[p] = static_cast<float>(h);
+  slope[2 * p] = static_cast<float>(d * per[0]);
+  slope[2 * p + 1] = static_cast<float>(-d * per[1]);
+}
+
+// The sequence that holds row t: the last one whose start is at or before it.
+__device__ __forceinline__ int64_t sequence_of(const int64_t* offsets, int64_t sequences, int64_t t) {
+  int64_t lo = 0, hi = sequences;  // offsets[lo] <= t < offsets[hi]
+  if (t < offsets[0] || t >= offsets[sequences]) return -1;
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) / 2;
+    if (offsets[mid] <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+template <int TY>
+__global__ __launch_bounds__(kThreads) void row_grad_kernel(const typename Elem<TY>::type* logits, int64_t vocab,
+                                                           int64_t stride, const int64_t* __restrict__ labels,
+                                                           const int64_t* __restrict__ offsets, int64_t sequences,
+                                                           const float2* __restrict__ stats, const float* __restrict__ slope,
+                                                           const float* __restrict__ grad_loss,
+                                                           typename Elem<TY>::type* dlogits, int64_t out_stride) {
+  const int64_t t = blockIdx.x;
+  const int64_t label = labels[t];
+  const int64_t seq = label < 0 ? -1 : sequence_of(offsets, sequences, t);
+  auto* out = dlogits + t * out_stride;
+  if (seq < 0) {
+    const float zero[8] = {};
+    for (int64_t c = static_cast<int64_t>(threadIdx.x) * 8; c < vocab; c += kThreads * 8) store8<TY>(out, c, vocab, zero);
+    return;
+  }
+  const auto* row = logits + t * stride;
+  const float2 st = stats[t];
+  float coef = slope[seq] * grad_loss[seq >> 1];
+  if (label >= vocab) coef = NAN;
+  const float base = st.x == -INFINITY ? 0.f : st.x;
+  const float k = -coef * st.y;
+  for (int64_t c = static_cast<int64_t>(threadIdx.x) * 8; c < vocab; c += kThreads * 8) {
+    float v[8];
+    load8<TY>(row, c, vocab, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = exp_hw(v[i] - base) * k + (c + i == label ? coef : 0.f);
+    store8<TY>(out, c, vocab, v);
+  }
+}
+
+template <int TY>
+hipError_t stats_as(const void* logits, int64_t tokens, int64_t vocab, int64_t stride, const int64_t* labels, float* logps,
+                    double* logps64, float* stats, hipStream_t stream) {
+  hipLaunchKernelGGL((row_stats_kernel<TY>), dim3(static_cast<unsigned>(tokens)), dim3(kThreads), 0, stream,
+                     static_cast<const typename Elem<TY>::type*>(logits), vocab, stride, labels, logps, logps64,
+                     reinterpret_cast<float2*>(stats));
+  return hipGetLastError();
+}
+
+hipError_t launch_stats(int type, const void* logits, int64_t tokens, int64_t vocab, int64_t stride, const int64_t* labels,
+                        float* logps, double* logps64, float* stats, hipStream_t stream) {
+  if (tokens == 0) return hipSuccess;
+  if (type == kBF16) return stats_as<kBF16>(logits, tokens, vocab, stride, labels, logps, logps64, stats, stream);
+  if (type == kF16) return stats_as<kF16>(logits, tokens, vocab, stride, labels, logps, logps64, stats, stream);
+  return stats_as<kF32>(logits, tokens, vocab, stride, labels, logps, logps64, stats, stream);
+}
+
+template <int TY>
+hipError_t grad_as(const void* logits, int64_t tokens, int64_t vocab, int64_t stride, const int64_t* labels,
+                   const int64_t* offsets, int64_t pairs, const float* stats, const float* slope, const float* grad_loss,
+                   void* dlogits, int64_t out_stride, hipStream_t stream) {
+  hipLaunchKernelGGL((row_grad_kernel<TY>), dim3(static_cast<unsigned>(tokens)), dim3(kThreads), 0, stream,
+                     static_cast<const typename Elem<TY>::type*>(logits), vocab, stride, labels, offsets, 2 * pairs,
+                     reinterpret_cast<const float2*>(stats), slope, grad_loss,
+                     static_cast<typename Elem<TY>::type*>(dlogits), out_stride);
+  return hipGetLastError();
+}
+
+// rows are workgroups: fewer than 2^32 threads a launch
+constexpr int64_t kMaxTokens = (int64_t{1} << 32) / kThreads - 1;
+
+const char* bad_logits(const void* logits, int type, int64_t tokens, int64_t vocab, int64_t stride, const int64_t* labels) {
+  if (const char* why = bad_matrix(tokens, vocab, stride, type)) return why;
+  if (tokens > kMaxTokens) return "too many tokens";
+  if (tokens > 0 && (!logits || !labels)) return "NULL logits or labels";
+  return nullptr;
+}
+
+}  // namespace
+}  // namespace mx
+}  // namespace casgd
+
+using namespace casgd;
+
+extern "C" {
+
+int casgd_token_logps(const void* logits, int type, int64_t tokens, int64_t vocab, int64_t stride, const int64_t* labels,
+                      float* logps, void* hip_stream) {
+  if (const char* why = mx::bad_logits(logits, type, tokens, vocab, stride, labels)) return api_fail(CASGD_EINVAL, why);
+  if (tokens > 0 && !logps) return api_fail(CASGD_EINVAL, "NULL logps");
+  const hipError_t e = mx::launch_stats(type, logits, tokens, vocab, stride, labels, logps, nullptr, nullptr,
+                                        static_cast<hipStream_t>(hip_stream));
+  return e == hipSuccess ? CASGD_OK : api_hip_fail(e, "token log probability launch");
+}
+
+int64_t casgd_pref_workspace(int64_t tokens) { return tokens < 0 || tokens > mx::kMaxTokens ? -1 : tokens * 8; }
+
+int casgd_pref_loss(const void* logits, int type, int64_t tokens, int64_t vocab, int64_t stride, const int64_t* labels,
+                    const int64_t* offsets, int64_t pairs, const float* ref_logps, int loss_kind, float beta,
+                    float smoothing, int average, float* loss, float* margin, float* logps, float* stats, float* slope,
+                    void* workspace, int64_t workspace_bytes, void* hip_stream) {
+  if (const char* why = mx::bad_logits(logits, type, tokens, vocab, stride, labels)) return api_fail(CASGD_EINVAL, why);
+  if (pairs < 1 || pairs > mx::kMaxTokens) return api_fail(CASGD_EINVAL, "pairs out of range");
+  if (loss_kind != CASGD_LOGISTIC && loss_kind != CASGD_SQUARED)
+    return api_fail(CASGD_EINVAL, "the preference loss is logistic or squared");
+  if (!(beta > 0.f) || !(beta < INFINITY)) return api_fail(CASGD_EINVAL, "beta must be positive and finite");
+  if (!(smoothing >= 0.f && smoothing <= 1.f)) return api_fail(CASGD_EINVAL, "smoothing must be in [0, 1]");
+  if (smoothing != 0.f && loss_kind != CASGD_LOGISTIC) return api_fail(CASGD_EINVAL, "smoothing is of the logistic loss");
+  if (!offsets || !loss || !margin || !slope || (tokens > 0 && (!logps || !stats || !workspace)))
+    return api_fail(CASGD_EINVAL, "NULL pointer");
+  if (reinterpret_cast<uintptr_t>(stats) % 8 != 0 || reinterpret_cast<uintptr_t>(workspace) % 8 != 0)
+    return api_fail(CASGD_EINVAL, "stats and workspace must be 8-byte aligned");
+  if (workspace_bytes < casgd_pref_workspace(tokens)) return api_fail(CASGD_EINVAL, "workspace too small");
+  hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+  double* logps64 = static_cast<double*>(workspace);
+  hipError_t e = mx::launch_stats(type, logits, tokens, vocab, stride, labels, logps, logps64, stats, stream);
+  if (e == hipSuccess) {
+    hipLaunchKernelGGL(mx::pair_kernel, dim3(static_cast<unsigned>(pairs)), dim3(mx::kThreads), 0, stream, logps64, ref_logps,
+                       labels, offsets, tokens, loss_kind, beta, smoothing, average, loss, margin, slope);
+    e = hipGetLastError();
+  }
+  return e == hipSuccess ? CASGD_OK : api_hip_fail(e, "preference loss launch");
+}
+
+int casgd_pref_grad(const void* logits, int type, int64_t tokens, int64_t vocab, int64_t stride, const int64_t* labels,
+                    const int64_t* offsets, int64_t pairs, const float* stats, const float* slope, const float* grad_loss,
+                    void* dlogits, int64_t out_stride, void* hip_stream) {
+  if (const char* why = mx::bad_logits(logits, type, tokens, vocab, stride, labels)) return api_fail(CASGD_EINVAL, why);
+  if (const char* why = mx::bad_matrix(tokens, vocab, out_stride, type)) return api_fail(CASGD_EINVAL, why);
+  if (pairs < 1 || pairs > mx::kMaxTokens) return api_fail(CASGD_EINVAL, "pairs out of range");
+  if (tokens == 0) return CASGD_OK;
+  if (!offsets || !stats || !slope || !grad_loss || !dlogits) return api_fail(CASGD_EINVAL, "NULL pointer");
+  if (reinterpret_cast<uintptr_t>(stats) % 8 != 0) return api_fail(CASGD_EINVAL, "stats must be 8-byte aligned");
+  hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+  hipError_t e;
+  if (type == mx::kBF16)
+    e = mx::grad_as<mx::kBF16>(logits, tokens, vocab, stride, labels, offsets, pairs, stats, slope, grad_loss, dlogits,
+                               out_stride, stream);
+  else if (type == mx::kF16)
+    e = mx::grad_as<mx::kF16>(logits, tokens, vocab, stride, labels, offsets, pairs, stats, slope, grad_loss, dlogits,
+                              out_stride, stream);
+  else
+    e = mx::grad_as<mx::kF32>(logits, tokens, vocab, stride, labels, offsets, pairs, stats, slope, grad_loss, dlogits,
+                              out_stride, stream);
+  return e == hipSuccess ? CASGD_OK : api_hip_fail(e, "preference gradient launch");
+}
+
+}  // extern "C"

@@ -311,6 +311,110 @@ int casgd_peak_copy(const void* src, void* dst, int64_t bytes, void* hip_stream)
 int casgd_peak_read(const void* src, int64_t bytes, float* out, int workgroups, void* hip_stream);
 int casgd_peak_mfma(float* out, int workgroups, int iters, void* hip_stream);
 
+/* ------------------------------------------------------------------------
+ * Operators of a low-precision linear layer and its preference loss.
+ *
+ * The precision choices above, for a layer with many outputs: weights kept in
+ * 4 bits, activations checkpointed in 8 bits, products with float32 sums, and
+ * the logistic or squared loss of a pair's margin.  These calls need no
+ * handle: they queue on hip_stream (NULL: the null stream) of the current
+ * device and return without waiting, allocate nothing and can be captured in a
+ * graph.  Element types are CASGD_BF16, CASGD_FP32 and CASGD_FP16; matrices
+ * are row-major with a row stride in elements (at least the columns) and may
+ * start at any element.  Outputs must not overlap inputs unless stated.
+ * Rows may be 0: such a call does nothing.  NaN and Inf propagate.
+ *
+ * Microscaled matrices.  A row of `cols` elements is padded with zeros to
+ * ld = casgd_mx_ld(cols), a multiple of 128, and cut into blocks of 32.
+ *   CASGD_MX4  E2M1 elements (0, .5, 1, 1.5, 2, 3, 4, 6): codes
+ *              uint8 [rows][ld / 2], the even element in the low nibble
+ *   CASGD_MX8  OCP E4M3 elements: codes uint8 [rows][ld]
+ *   scales     uint8 [rows][ld / 32]: element = code value * 2^(scale - 127)
+ * The scale is the least power of two (byte 1 ... 254) for which the block's
+ * max |x| / scale is at most 6 (MX4) or 448 (MX8), as the fp8 storage's
+ * exponent is chosen per matrix; elements are rounded to nearest even and
+ * never saturate.  A block that holds a NaN or an infinity has scale byte 255
+ * and stands for NaN.  codes must be 16-byte aligned, scales 4-byte.
+ */
+enum casgd_mx_format { CASGD_MX4 = 0, CASGD_MX8 = 1 };
+
+/* Padded row length of a microscaled matrix; -1 for cols out of range. */
+int64_t casgd_mx_ld(int64_t cols);
+
+/* x (rows x cols) to codes and scales, padding included, and back to the
+ * nearest values of `type` (an 8-bit value of a block may need more range
+ * than fp16 has). */
+int casgd_mx_quantize(const void* x, int type, int64_t rows, int64_t cols, int64_t stride, int format, uint8_t* codes,
+                      uint8_t* scales, void* hip_stream);
+int casgd_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int format, int64_t rows, int64_t cols, void* out,
+                        int type, int64_t stride, void* hip_stream);
+
+/* y = Q4(x) W^T: x (m x k) is quantised to MX4 as by casgd_mx_quantize, W
+ * (n x k) is kept in MX4; float32 sums, rounded once to y's type (m x n).
+ * workspace: device memory of casgd_mx4_linear_workspace(m, k, n) bytes, at
+ * least, 16-byte aligned, free again when the call's work is done.
+ * Bit-identical on repeats. */
+int64_t casgd_mx4_linear_workspace(int64_t m, int64_t k, int64_t n);
+int casgd_mx4_linear(const void* x, int x_type, int64_t m, int64_t k, int64_t x_stride, const uint8_t* w_codes,
+                     const uint8_t* w_scales, int64_t n, void* y, int y_type, int64_t y_stride, void* workspace,
+                     int64_t workspace_bytes, void* hip_stream);
+
+/* The layer's backward pass.  The gradient dy (m x n) is used as it is (a
+ * float32 one is not rounded), sums are float32, the result is rounded once.
+ *   casgd_mx4_grad_input   dx (m x k) = dy W, W (n x k) in MX4
+ *   casgd_mx8_grad_weight  dW (n x k) = dy^T X, X (t x k) the activations
+ *                          checkpointed in MX8 (the rounding of Q4 taken as
+ *                          the identity); accumulate != 0 adds to dw.  t = 0
+ *                          gives zeros (or leaves dw). */
+int casgd_mx4_grad_input(const void* dy, int dy_type, int64_t m, int64_t n, int64_t dy_stride, const uint8_t* w_codes,
+                         const uint8_t* w_scales, int64_t k, void* dx, int dx_type, int64_t dx_stride, void* hip_stream);
+int casgd_mx8_grad_weight(const void* dy, int dy_type, int64_t t, int64_t n, int64_t dy_stride, const uint8_t* x_codes,
+                          const uint8_t* x_scales, int64_t k, void* dw, int dw_type, int64_t dw_stride, int accumulate,
+                          void* hip_stream);
+
+/* Log probabilities of the labelled tokens: logps[t] = z_t[y_t] -
+ * log sum_v exp z_t[v], float32, from logits z (tokens x vocab).
+ *   labels  device, int64 [tokens]; a negative label masks its row (0, the
+ *           row is not read); a label >= vocab gives NaN. */
+int casgd_token_logps(const void* logits, int type, int64_t tokens, int64_t vocab, int64_t stride, const int64_t* labels,
+                      float* logps, void* hip_stream);
+
+/*
+ * Preference loss of paired log ratios (Bradley-Terry margin of a policy
+ * against a reference).  Pair p's chosen tokens are rows [offsets[2p],
+ * offsets[2p+1]), its rejected ones [offsets[2p+1], offsets[2p+2]); masked
+ * tokens are left out, an empty sequence sums to 0.
+ *   h = sum_chosen (logps - ref) - sum_rejected (logps - ref), each sum
+ *       divided by its count of unmasked tokens if average != 0
+ *   CASGD_LOGISTIC  (1 - smoothing) log(1 + exp(-beta h))
+ *                   + smoothing log(1 + exp(beta h))
+ *   CASGD_SQUARED   (h - 1 / (2 beta))^2
+ *   offsets    device, int64 [2 pairs + 1], not decreasing; values are
+ *              clamped to [0, tokens]; rows outside belong to no pair
+ *   ref_logps  device, float32 [tokens] (casgd_token_logps of the reference
+ *              model), or NULL for zeros
+ *   loss, margin (h)  device, float32 [pairs]
+ *   logps      device, float32 [tokens]
+ *   stats      device, float32 [tokens][2], 8-byte aligned: kept for the
+ *              gradient (max and 1 / sum of the row's softmax)
+ *   slope      device, float32 [2 pairs]: d loss / d logps of each sequence
+ *   workspace  casgd_pref_workspace(tokens) bytes, 8-byte aligned
+ * Sums over tokens are float64 in a fixed order.
+ */
+int64_t casgd_pref_workspace(int64_t tokens);
+int casgd_pref_loss(const void* logits, int type, int64_t tokens, int64_t vocab, int64_t stride, const int64_t* labels,
+                    const int64_t* offsets, int64_t pairs, const float* ref_logps, int loss_kind, float beta,
+                    float smoothing, int average, float* loss, float* margin, float* logps, float* stats, float* slope,
+                    void* workspace, int64_t workspace_bytes, void* hip_stream);
+
+/* Gradient of sum_p grad_loss[p] * loss[p] in the logits, of their type;
+ * stats and slope are casgd_pref_loss's.  Rows that are masked or belong to
+ * no pair get zeros and are not read.  dlogits may be logits itself, with the
+ * same stride. */
+int casgd_pref_grad(const void* logits, int type, int64_t tokens, int64_t vocab, int64_t stride, const int64_t* labels,
+                    const int64_t* offsets, int64_t pairs, const float* stats, const float* slope, const float* grad_loss,
+                    void* dlogits, int64_t out_stride, void* hip_stream);
+
 /* Text of the last error on the calling thread ("" if none). */
 const char* casgd_last_error(void);
 

@@ -1,0 +1,274 @@
+"""Microscaled storage and products on the GPU against the float64 oracle.
+
+Codes and scales are compared bit for bit.  A product of stored values is held
+to Higham's order-free bound of its float32 sums, gamma_k sum|a||b| with
+gamma_k = k u / (1 - k u) and u = 2^-23, plus half a step of the output's
+type, eps / 2 of the value, and half its least subnormal."""
+
+import numpy as np
+import pytest
+import torch
+
+from communication_avoiding_mixed_amd import binding as B
+from oracle import head_oracle as H
+
+pytestmark = pytest.mark.gpu
+
+T = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+ULP0 = {"bf16": 0.0, "fp16": 2.0 ** -25, "fp32": 0.0}
+
+
+def cuda(a, dtype="fp32"):
+    return torch.from_numpy(np.ascontiguousarray(a, np.float32)).to(T[dtype]).cuda()
+
+
+def host(t):
+    return t.double().cpu().numpy()
+
+
+def values(shape, seed, spread=1.0):
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal(shape) * np.exp(spread * rng.standard_normal((shape[0], 1)))
+    x[:, rng.random(shape[1]) < 0.05] *= 12
+    x[:, rng.random(shape[1]) < 0.05] = 0
+    return x.astype(np.float32)
+
+
+def strided(t, extra, offset):
+    """The same matrix inside a wider one, at an odd element offset."""
+    big = torch.full((t.shape[0], t.shape[1] + extra), float("nan"), dtype=t.dtype, device=t.device)
+    view = big[:, offset:offset + t.shape[1]]
+    view.copy_(t)
+    return view
+
+
+def stored(x, fmt):
+    """MXMatrix from the oracle's own bytes."""
+    codes, scales = H.quantize(x, fmt)
+    return B.MXMatrix(fmt, torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), x.shape[1])
+
+
+def close(got, a, b, dtype, base=None):
+    """got against a @ b in float64 (plus base) elementwise."""
+    ref = a @ b
+    k = a.shape[1] + (0 if base is None else 1)
+    size = np.abs(a) @ np.abs(b)
+    if base is not None:
+        ref, size = ref + base, size + np.abs(base)
+    u = 2.0 ** -23
+    tol = k * u / (1 - k * u) * size
+    tol = tol + torch.finfo(T[dtype]).eps / 2 * (np.abs(ref) + tol) + ULP0[dtype]
+    bad = ~(np.abs(host(got) - ref) <= tol)
+    assert not bad.any(), (bad.sum(), np.argwhere(bad)[:5], host(got)[bad][:5], ref[bad][:5])
+
+
+SHAPES = [(1, 1), (1, 32), (3, 33), (5, 127), (4, 128), (2, 129), (7, 2000), (64, 300), (257, 65)]
+
+
+@pytest.mark.parametrize("dtype", list(T))
+@pytest.mark.parametrize("fmt", ["mx4", "mx8"])
+def test_quantise_is_bit_exact(fmt, dtype):
+    for i, shape in enumerate(SHAPES):
+        x = cuda(values(shape, i, 3.0), dtype)
+        codes, scales = H.quantize(host(x), fmt)
+        for view in (x, strided(x, 9, 3), strided(x, 1, 1)):
+            q = B.mx_quantize(view, fmt)
+            np.testing.assert_array_equal(q.scales.cpu().numpy(), scales)
+            np.testing.assert_array_equal(q.codes.cpu().numpy(), codes)
+        for out in T:
+            back = torch.from_numpy(H.dequantize(codes, scales, shape[1], fmt)).to(T[out]).double().numpy()
+            np.testing.assert_array_equal(host(B.mx_dequantize(q, T[out])), back)
+
+
+@pytest.mark.parametrize("fmt", ["mx4", "mx8"])
+def test_quantise_ties_extremes_and_non_finite_blocks(fmt):
+    rng = np.random.default_rng(3)
+    table = H.E2M1 if fmt == "mx4" else H.E4M3
+    mid = (table[1:] + table[:-1]) / 2
+    rows = []
+    for e in (-126, -100, -20, 0, 20, 100, 125 if fmt == "mx4" else 119):
+        for s in (1, -1):
+            r = np.zeros(128)
+            pick = np.concatenate([mid, mid * (1 + 2.0 ** -20), mid * (1 - 2.0 ** -20), table])
+            r[:96] = rng.choice(pick, 96) * s
+            r[::32] = table[-1]  # the block's scale is 2^e
+            rows.append(r * 2.0 ** e)
+    x = np.array(rows)
+    bad = np.tile(rng.standard_normal((1, 128)), (4, 1))
+    bad[0, 5], bad[1, 40], bad[2, 70], bad[3, 127] = np.nan, np.inf, -np.inf, np.nan
+    tiny = np.array([np.full(128, 1e-44), np.full(128, 2.0 ** -126), np.zeros(128), np.full(128, -0.0)])
+    x = np.concatenate([x, bad, tiny]).astype(np.float32)
+    codes, scales = H.quantize(x.astype(np.float64), fmt)
+    q = B.mx_quantize(torch.from_numpy(x).cuda(), fmt)
+    np.testing.assert_array_equal(q.scales.cpu().numpy(), scales)
+    np.testing.assert_array_equal(q.codes.cpu().numpy(), codes)
+    np.testing.assert_array_equal(host(B.mx_dequantize(q, torch.float32)),
+                                  H.dequantize(codes, scales, 128, fmt).astype(np.float32))
+
+
+LINEAR = [(1, 1, 1), (1, 32, 5), (1, 2000, 300), (2, 129, 64), (5, 640, 33), (15, 4096, 17), (16, 512, 16), (17, 96, 130),
+          (31, 256, 257), (33, 1000, 128), (64, 128, 64), (65, 160, 300), (100, 2000, 259), (128, 512, 256),
+          (129, 700, 127), (257, 384, 513), (300, 64, 1024)]
+
+
+@pytest.mark.parametrize("m,k,n", LINEAR)
+def test_linear(m, k, n):
+    w = stored(values((n, k), 7) / np.sqrt(k), "mx4")
+    wv = H.dequantize(w.codes.cpu().numpy(), w.scales.cpu().numpy(), k, "mx4")
+    for dtype, out in (("bf16", "bf16"), ("fp16", "fp32"), ("fp32", "fp16"), ("bf16", "fp32")):
+        x = cuda(values((m, k), 8, 0.5), dtype)
+        xv = H.rounded(host(x), "mx4")
+        got = B.mx4_linear(x, w, T[out])
+        close(got, xv, wv.T, out)
+        again = B.mx4_linear(strided(x, 5, 3), w, T[out])
+        assert torch.equal(got, again)  # the same bits, whatever the strides
+
+
+def test_linear_propagates_nan_blocks():
+    x, w = values((3, 256), 1), values((40, 256), 2)
+    x[1, 200], w[7, 3], w[9, 255] = np.inf, np.nan, -np.inf
+    y = host(B.mx4_linear(cuda(x), stored(w, "mx4")))
+    bad = np.zeros((3, 40), bool)
+    bad[1], bad[:, 7], bad[:, 9] = True, True, True
+    np.testing.assert_array_equal(np.isnan(y), bad)
+    x = np.tile(x, (100, 1))
+    y = host(B.mx4_linear(cuda(x), stored(w, "mx4")))
+    np.testing.assert_array_equal(np.isnan(y), np.tile(bad, (100, 1)))
+
+
+def test_linear_scales_over_the_whole_range():
+    # products of the largest and least scales stay finite or go to zero as float32 does
+    x, w = np.zeros((2, 64), np.float32), np.zeros((3, 64), np.float32)
+    x[0, :32], x[1, :32] = 2.0 ** 100, 2.0 ** -100
+    w[0, :32], w[1, :32], w[2, 32:] = 2.0 ** 20, 2.0 ** 25, 1.0
+    y = host(B.mx4_linear(cuda(x), stored(w, "mx4")))
+    np.testing.assert_array_equal(y, [[2.0 ** 125, np.inf, 0], [2.0 ** -75, 2.0 ** -70, 0]])
+
+
+GRAD = [(1, 1, 1), (1, 64, 70), (2, 130, 33), (31, 32, 64), (32, 300, 65), (33, 129, 200), (37, 1000, 500), (64, 64, 64),
+        (100, 257, 640), (128, 128, 256), (200, 520, 130), (513, 96, 100), (1500, 40, 33)]
+
+
+@pytest.mark.parametrize("m,n,k", GRAD)
+def test_gradients(m, n, k):
+    w, x = stored(values((n, k), 4), "mx4"), stored(values((m, k), 5), "mx8")
+    wv = H.dequantize(w.codes.cpu().numpy(), w.scales.cpu().numpy(), k, "mx4")
+    xv = H.dequantize(x.codes.cpu().numpy(), x.scales.cpu().numpy(), k, "mx8")
+    for dtype, out in (("bf16", "bf16"), ("bf16", "fp32"), ("fp16", "fp32"), ("fp32", "fp32"), ("fp32", "fp16"), ("fp16", "bf16")):
+        dy = cuda(values((m, n), 6) * 0.01, dtype)
+        dyv = host(dy)
+        got = B.mx4_grad_input(dy, w, T[out])
+        close(got, dyv, wv, out)
+        assert torch.equal(got, B.mx4_grad_input(strided(dy, 7, 1), w, T[out]))
+        got = B.mx8_grad_weight(dy, x, out_dtype=T[out])
+        close(got, dyv.T, xv, out)
+        wide = strided(torch.ones((n, k), dtype=T[out], device="cuda"), 3, 1)
+        B.mx8_grad_weight(strided(dy, 2, 1), x, out=wide, accumulate=True)
+        close(wide, dyv.T, xv, out, base=1.0)
+        assert torch.equal(got, B.mx8_grad_weight(strided(dy, 5, 3), x, out_dtype=T[out]))
+
+
+def test_gradient_of_no_rows():
+    x = B.mx_quantize(torch.empty((0, 40), device="cuda"), "mx8")
+    dy = torch.empty((0, 6), device="cuda")
+    assert not B.mx8_grad_weight(dy, x).any()
+    kept = torch.full((6, 40), 3.0, device="cuda")
+    assert (B.mx8_grad_weight(dy, x, out=kept, accumulate=True) == 3).all()
+    w = stored(values((6, 40), 1), "mx4")
+    assert B.mx4_grad_input(dy, w).shape == (0, 40) and B.mx4_linear(torch.empty((0, 40), device="cuda"), w).shape == (0, 6)
+
+
+def test_gradients_propagate_non_finite():
+    dy, w, x = values((70, 90), 1), values((90, 100), 2), values((70, 100), 3)
+    dy[3, 4], w[5, 60], x[6, 99] = np.inf, np.nan, np.nan
+    dx = host(B.mx4_grad_input(cuda(dy), stored(w, "mx4")))
+    want = np.zeros((70, 100), bool)
+    want[3], want[:, 32:64] = True, True
+    np.testing.assert_array_equal(~np.isfinite(dx), want)
+    dw = host(B.mx8_grad_weight(cuda(dy, "bf16"), stored(x, "mx8")))
+    want = np.zeros((90, 100), bool)
+    want[4], want[:, 96:] = True, True
+    np.testing.assert_array_equal(~np.isfinite(dw), want)
+
+
+def test_backward_against_differences_of_the_forward():
+    # the forward is linear in W's stored values: a unit step in one of them changes y by Q4(x)'s column
+    x = H.rounded(values((6, 64), 1, 0.0), "mx4").astype(np.float32)  # a fixed point of Q4, and of Q8 where it holds it
+    w, dy = H.rounded(values((5, 64), 2, 0.0), "mx4"), values((6, 5), 3, 0.0)
+    y0 = host(B.mx4_linear(cuda(x), stored(w, "mx4"), torch.float32))
+    dw = host(B.mx8_grad_weight(cuda(dy), B.mx_quantize(cuda(x), "mx8")))
+    dx = host(B.mx4_grad_input(cuda(dy), stored(w, "mx4")))
+    assert np.array_equal(H.rounded(x, "mx8"), x)
+    for n, k in ((0, 0), (4, 63), (2, 31)):
+        w1 = w.copy()
+        w1[n, k] = -w[n, k] if w[n, k] else 0.5 * 2.0 ** (int(H.quantize(w, "mx4")[1][n, k // 32]) - 127)
+        step = w1[n, k] - w[n, k]
+        y1 = host(B.mx4_linear(cuda(x), stored(w1, "mx4"), torch.float32))
+        # both products are exact up to 64 float32 roundings
+        assert abs(((y1 - y0) * dy).sum() / step - dw[n, k]) <= 300 * 2.0 ** -23 * (np.abs(dy[:, n]) @ (np.abs(y0[:, n]) + np.abs(x[:, k]) * abs(step))) / abs(step)
+    for m, k in ((0, 0), (5, 40)):
+        x1 = x.copy()
+        x1[m, k] = -x[m, k] if x[m, k] else 0.5 * 2.0 ** (int(H.quantize(x, "mx4")[1][m, k // 32]) - 127)
+        step = x1[m, k] - x[m, k]
+        y1 = host(B.mx4_linear(cuda(x1), stored(w, "mx4"), torch.float32))
+        assert abs(((y1 - y0) * dy).sum() / step - dx[m, k]) <= 300 * 2.0 ** -23 * (np.abs(dy[m]) @ (np.abs(y0[m]) + np.abs(w[:, k]) * abs(step))) / abs(step)
+
+
+def test_side_stream_and_graph_replays():
+    x = torch.randn(40, 320, device="cuda").bfloat16()
+    w = stored(values((200, 320), 1), "mx4")
+    dy = torch.randn(40, 200, device="cuda").bfloat16()
+
+    def step():
+        q = B.mx_quantize(x, "mx8")
+        return B.mx4_linear(x, w), B.mx4_grad_input(dy, w), B.mx8_grad_weight(dy, q), B.mx_dequantize(q, torch.bfloat16)
+
+    eager = step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = step()
+    torch.cuda.current_stream().wait_stream(side)
+    for a, b in zip(eager, other):
+        assert torch.equal(a, b)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for i in range(4):
+        x.copy_(torch.randn(40, 320, device="cuda").bfloat16())
+        dy.copy_(torch.randn(40, 200, device="cuda").bfloat16())
+        graph.replay()
+        eager = step()
+        torch.cuda.synchronize()
+        for a, b in zip(eager, captured):
+            assert torch.equal(a, b)
+
+
+def test_binding_refusals():
+    x = torch.zeros(4, 64, device="cuda")
+    w = stored(values((8, 64), 1), "mx4")
+    with pytest.raises(ValueError, match="mx4"):
+        B.mx4_linear(x, stored(values((8, 64), 1), "mx8"))
+    with pytest.raises(ValueError, match="columns"):
+        B.mx4_linear(torch.zeros(4, 65, device="cuda"), w)
+    with pytest.raises(ValueError, match="contiguous rows"):
+        B.mx4_linear(torch.zeros(64, 4, device="cuda").t(), w)
+    with pytest.raises(ValueError, match="contiguous rows"):
+        B.mx_quantize(torch.zeros(1, 64, device="cuda").expand(4, 64), "mx4")
+    with pytest.raises(ValueError, match="2-D"):
+        B.mx_quantize(x[0], "mx4")
+    with pytest.raises(ValueError, match="bfloat16"):
+        B.mx_quantize(x.double(), "mx4")
+    with pytest.raises(ValueError, match="fmt"):
+        B.mx_quantize(x, "mx6")
+    with pytest.raises(ValueError, match="rows"):
+        B.mx4_grad_input(x, w)
+    with pytest.raises(ValueError, match="rows"):
+        B.mx8_grad_weight(torch.zeros(5, 8, device="cuda"), B.mx_quantize(x, "mx8"))
+    with pytest.raises(ValueError, match="accumulate"):
+        B.mx8_grad_weight(torch.zeros(4, 8, device="cuda"), B.mx_quantize(x, "mx8"), accumulate=True)
+    with pytest.raises(ValueError, match="out must"):
+        B.mx8_grad_weight(torch.zeros(4, 8, device="cuda"), B.mx_quantize(x, "mx8"), out=torch.zeros(8, 63, device="cuda"))
+    with pytest.raises(ValueError, match="uint8"):
+        B.MXMatrix("mx4", w.codes.to(torch.int32), w.scales, 64)

@@ -1,0 +1,97 @@
+"""Refusals of the low-precision linear layer's entry points that need no GPU:
+the C ABI checks its arguments on the host before anything is queued."""
+
+import ctypes
+
+import pytest
+import torch
+
+from communication_avoiding_mixed_amd import binding as B
+
+P = ctypes.c_void_p(4096)  # an aligned address that no refused call reads
+ODD = ctypes.c_void_p(4097)
+
+
+def refused(rc, text):
+    assert rc == B.EINVAL
+    assert text in B.load().casgd_last_error().decode()
+
+
+def test_padded_row_length():
+    lib = B.load()
+    assert [lib.casgd_mx_ld(c) for c in (1, 128, 129, 2000)] == [128, 128, 256, 2048]
+    assert [B.mx_ld(c) for c in (1, 128, 129, 2000)] == [128, 128, 256, 2048]
+    assert lib.casgd_mx_ld(0) == -1 and lib.casgd_mx_ld(2 ** 31) == -1
+
+
+@pytest.mark.parametrize("args,text", [
+    ((P, B.FP8, 4, 64, 64, B.MX4, P, P), "element type"),
+    ((P, B.BF16, -1, 64, 64, B.MX4, P, P), "rows out of range"),
+    ((P, B.BF16, 4, 0, 64, B.MX4, P, P), "columns out of range"),
+    ((P, B.BF16, 4, 64, 63, B.MX4, P, P), "row stride"),
+    ((P, B.BF16, 4, 64, 64, 2, P, P), "format"),
+    ((None, B.BF16, 4, 64, 64, B.MX4, P, P), "NULL"),
+    ((P, B.BF16, 4, 64, 64, B.MX4, None, P), "NULL"),
+    ((P, B.BF16, 4, 64, 64, B.MX4, P, None), "NULL"),
+    ((P, B.BF16, 4, 64, 64, B.MX4, ODD, P), "aligned"),
+    ((P, B.BF16, 4, 64, 64, B.MX8, P, ODD), "aligned")])
+def test_quantise_refusals(args, text):
+    x, ty, rows, cols, stride, fmt, codes, scales = args
+    refused(B.load().casgd_mx_quantize(*args, None), text)
+    refused(B.load().casgd_mx_dequantize(codes, scales, fmt, rows, cols, x, ty, stride, None), text)
+
+
+def test_product_refusals():
+    lib = B.load()
+    need = lib.casgd_mx4_linear_workspace(4, 64, 8)
+    assert need > 0 and lib.casgd_mx4_linear_workspace(4, 0, 8) == -1
+    ok = (P, B.BF16, 4, 64, 64, P, P, 8, P, B.BF16, 8, P, need, None)
+
+    def linear(at, value, text):
+        refused(lib.casgd_mx4_linear(*ok[:at], value, *ok[at + 1:]), text)
+
+    linear(0, None, "NULL"), linear(8, None, "NULL"), linear(11, None, "NULL"), linear(5, None, "NULL")
+    linear(1, 3, "element type"), linear(9, 7, "element type"), linear(4, 63, "row stride"), linear(10, 7, "row stride")
+    linear(12, need - 1, "workspace"), linear(11, ODD, "aligned"), linear(5, ODD, "aligned"), linear(7, 0, "columns")
+    refused(lib.casgd_mx4_grad_input(P, B.FP32, 4, 8, 7, P, P, 64, P, B.FP32, 64, None), "row stride")
+    refused(lib.casgd_mx4_grad_input(None, B.FP32, 4, 8, 8, P, P, 64, P, B.FP32, 64, None), "NULL")
+    refused(lib.casgd_mx4_grad_input(P, B.FP32, 4, 8, 8, P, P, 64, P, B.FP8, 64, None), "element type")
+    refused(lib.casgd_mx8_grad_weight(P, B.FP32, 4, 8, 8, P, P, 64, None, B.FP32, 64, 0, None), "NULL")
+    refused(lib.casgd_mx8_grad_weight(P, B.FP32, 4, 8, 8, P, P, 64, P, B.FP32, 63, 0, None), "row stride")
+    refused(lib.casgd_mx8_grad_weight(P, B.FP32, 4, 8, 8, None, P, 64, P, B.FP32, 64, 0, None), "NULL")
+
+
+def test_preference_refusals():
+    lib = B.load()
+    assert lib.casgd_pref_workspace(10) == 80 and lib.casgd_pref_workspace(-1) == -1
+    ok = [P, B.FP32, 6, 9, 9, P, P, 1, None, B.LOGISTIC, 0.1, 0.0, 0, P, P, P, P, P, P, 48, None]
+
+    def loss(at, value, text):
+        refused(lib.casgd_pref_loss(*ok[:at], value, *ok[at + 1:]), text)
+
+    for at in (0, 5, 6, 13, 14, 15, 16, 17, 18):
+        loss(at, None, "NULL")
+    loss(1, B.FP8, "element type"), loss(4, 8, "row stride"), loss(7, 0, "pairs"), loss(9, B.POISSON, "logistic or squared")
+    loss(10, 0.0, "beta"), loss(10, float("nan"), "beta"), loss(10, float("inf"), "beta"), loss(11, 1.5, "smoothing")
+    loss(16, ODD, "aligned"), loss(19, 47, "workspace"), loss(2, 2 ** 30, "tokens")
+    ok[9], ok[11] = B.SQUARED, 0.1
+    refused(lib.casgd_pref_loss(*ok), "smoothing")
+    refused(lib.casgd_token_logps(P, B.FP32, 6, 9, 9, None, P, None), "NULL")
+    refused(lib.casgd_token_logps(P, B.FP32, 6, 9, 9, P, None, None), "NULL")
+    refused(lib.casgd_pref_grad(P, B.FP32, 6, 9, 9, P, P, 1, P, P, None, P, 9, None), "NULL")
+    refused(lib.casgd_pref_grad(P, B.FP32, 6, 9, 9, P, P, 1, P, P, P, P, 8, None), "row stride")
+    refused(lib.casgd_pref_grad(P, B.FP32, 6, 9, 9, P, P, 0, P, P, P, P, 9, None), "pairs")
+
+
+def test_host_tensors_are_refused():
+    x = torch.zeros(4, 64)
+    with pytest.raises(ValueError, match="GPU"):
+        B.mx_quantize(x, "mx4")
+    with pytest.raises(ValueError, match="GPU"):
+        B.MXMatrix("mx4", torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, 4, dtype=torch.uint8), 64)
+    with pytest.raises(ValueError, match="fit"):
+        B.MXMatrix("mx4", torch.zeros(4, 60, dtype=torch.uint8), torch.zeros(4, 4, dtype=torch.uint8), 64)
+    with pytest.raises(ValueError, match="GPU"):
+        B.token_logps(x, torch.zeros(4, dtype=torch.int64))
+    with pytest.raises(ValueError, match="loss"):
+        B.pref_loss(x, None, None, loss="poisson")
