@@ -1,0 +1,443 @@
+// Product of two MX4 matrices, y[m][n] = sum_k X[m][k] W[n][k], on the scaled
+// matrix instructions (32x32x64 f8f6f4 with E2M1 operands): an operand's lane
+// holds one whole block of 32 elements (16 bytes) and its scale byte, so the
+// stored form feeds the instruction as it is.
+//
+// The summed index may be permuted as long as both operands agree.  A stage
+// is 128 elements of each row: 4 blocks.  Instruction s (0, 1) of a stage takes
+// block s in lanes 0-31 and block 2 + s in lanes 32-63, so a lane's two scale
+// bytes are neighbours and a lane's two 16-byte pieces too.
+#pragma once
+
+#include "casgd_mx.h"
+
+namespace casgd {
+namespace mx {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// vmcnt(n) alone: the other counters at their maximum
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+__device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (3 << 14)); }
+
+// Direct-to-LDS load, 16 bytes a lane: lane i's bytes at base + off go to LDS
+// at lds + 16 i.  No register result; the data is there after this wave's
+// vmcnt has counted it.  Written as asm because the compiler makes every later
+// LDS read of the wave wait for all loads of this kind that it knows of, which
+// would leave one stage in flight; the waits here are explicit.
+__device__ __forceinline__ void load_lds16(uint32_t lds, const void* base, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+}
+
+__device__ __forceinline__ f32x16 mfma_mx4_32(i32x4 a, i32x4 b, f32x16 c, int sa, int sb, int which) {
+  const i32x8 a8 = {a.x, a.y, a.z, a.w, 0, 0, 0, 0}, b8 = {b.x, b.y, b.z, b.w, 0, 0, 0, 0};
+  switch (which) {
+    case 0: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, 0, sa, 0, sb);
+    case 1: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, 1, sa, 1, sb);
+    case 2: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, 2, sa, 2, sb);
+    default: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, 3, sa, 3, sb);
+  }
+}
+
+// Tile (bm, bn) of workgroup `id` in a tiles_m x tiles_n grid.  Dispatch deals
+// workgroups to the 8 XCDs in turn; each XCD gets one run of consecutive
+// tiles, walked in bands of `band` tile rows, so that the tiles in flight on
+// an XCD share rows of both operands in its L2.
+__device__ __forceinline__ void tile_of(uint32_t id, uint32_t tiles_m, uint32_t tiles_n, uint32_t band, uint32_t& bm,
+                                        uint32_t& bn) {
+  const uint32_t total = tiles_m * tiles_n, xcds = 8;
+  const uint32_t x = id % xcds, i = id / xcds;
+  const uint32_t per = total / xcds, extra = total % xcds;
+  const uint32_t t = x * per + (x < extra ? x : extra) + i;
+  const uint32_t b = t / (band * tiles_n);
+  const uint32_t rows = tiles_m - b * band < band ? tiles_m - b * band : band;
+  const uint32_t in = t - b * band * tiles_n;
+  bm = b * band + in % rows;
+  bn = in / rows;
+}
+
+struct Mx4Operand {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int64_t rows;
+};
+
+// LDS of a tile: four stages of codes and two buffers of scales, 16 bytes
+// (four stages) a row
+template <int RX, int RW>
+constexpr int gemm_lds_bytes() {
+  return (RX + RW) * (4 * 64 + 2 * 16);
+}
+
+// One RX x RW tile (rows of x by rows of W) of y by GM x GN waves.
+//
+// Codes travel through a ring of four stages by direct-to-LDS loads, three
+// stages ahead; a row's 64 bytes are four 16-byte pieces, stored at piece
+// number XOR (row / 2 mod 4), so that 8 lanes reading one piece of 8 rows touch
+// all banks.  Fragments are read half a stage ahead of their instructions, and
+// the barrier that frees a ring slot sits between the halves, behind queued
+// matrix work.
+//
+// W is the instruction's A operand: a lane ends with 4 consecutive n of one m,
+// which go through LDS to full-width row stores.
+template <int OUT, int RX, int RW, int GM, int GN>
+__global__ __launch_bounds__(64 * GM * GN, 2) void mx4_gemm_kernel(Mx4Operand x, Mx4Operand w, int64_t ld,
+                                                         typename Elem<OUT>::type* __restrict__ y, int64_t stride,
+                                                         uint32_t tiles_m, uint32_t tiles_n, uint32_t band) {
+  constexpr int WM = RX / GM / 32, WN = RW / GN / 32;  // 32 x 32 results of a wave
+  constexpr int ROWS = RW + RX, WAVES = GM * GN;
+  constexpr int STAGE = ROWS * 64, SCALES = 4 * STAGE, SBUF = ROWS * 16;
+  constexpr int NC = ROWS / 16 / WAVES;  // 16-row code loads of a wave per stage
+  constexpr int NS = ROWS / 64 / WAVES;  // 64-row scale loads of a wave per four stages
+  static_assert(ROWS % (64 * WAVES) == 0 && RW % 64 == 0, "whole loads");
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint32_t bm, bn;
+  tile_of(blockIdx.x, tiles_m, tiles_n, band, bm, bn);
+  const int64_t m0 = static_cast<int64_t>(bm) * RX, n0 = static_cast<int64_t>(bn) * RW;
+  const int stages = static_cast<int>(ld / 128);
+  const int64_t cpitch = ld / 2, spitch = ld / 32;
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)smem));
+
+  // rows past the matrix read its last row; they only feed outputs that are
+  // not stored
+  const uint8_t* cbase[NC];
+  uint32_t coff[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int g = wave * NC + i;
+    const bool is_w = g < RW / 16;
+    const int first = is_w ? g * 16 : g * 16 - RW;
+    const int64_t left = is_w ? w.rows - n0 : x.rows - m0;
+    int r = first + (lane >> 2);
+    const int piece = (lane & 3) ^ ((r >> 1) & 3);
+    if (r >= left) r = static_cast<int>(left) - 1;
+    cbase[i] = is_w ? w.codes + n0 * cpitch : x.codes + m0 * cpitch;
+    coff[i] = static_cast<uint32_t>(r * cpitch) + piece * 16;
+  }
+  const uint8_t* sbase[NS];
+  uint32_t soff[NS];
+  uint32_t send[NS];  // bytes from the base to the matrix's end
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    const int g = wave * NS + i;
+    const bool is_w = g < RW / 64;
+    const int first = is_w ? g * 64 : g * 64 - RW;
+    const int64_t left = is_w ? w.rows - n0 : x.rows - m0;
+    int r = first + lane;
+    if (r >= left) r = static_cast<int>(left) - 1;
+    sbase[i] = is_w ? w.scales + n0 * spitch : x.scales + m0 * spitch;
+    soff[i] = static_cast<uint32_t>(r * spitch);
+    const int64_t end = left * spitch;
+    send[i] = end > 0xFFFFFFFFll ? 0xFFFFFFFFu : static_cast<uint32_t>(end);
+  }
+  auto load_codes = [&](int st) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      load_lds16(lds0 + (st & 3) * STAGE + (wave * NC + i) * 1024, cbase[i] + static_cast<int64_t>(st) * 64, coff[i]);
+  };
+  // Scales of stages 4q .. 4q + 3.  A row's 16 bytes may run into the next row
+  // (bytes that no stage uses) but not past the matrix: the last rows' last
+  // piece is copied by words.
+  auto load_scales = [&](int q) {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const uint32_t to = SCALES + (q & 1) * SBUF + (wave * NS + i) * 1024;
+      const uint32_t at = soff[i] + q * 16;
+      if (at + 16 <= send[i]) {
+        load_lds16(lds0 + to, sbase[i], at);
+      } else {
+#pragma unroll
+        for (int b = 0; b < 16; b += 4)
+          if (at + b + 4 <= send[i])
+            *reinterpret_cast<uint32_t*>(smem + to + lane * 16 + b) = *reinterpret_cast<const uint32_t*>(sbase[i] + at + b);
+      }
+    }
+  };
+
+  const int wn = wave / GM, wm = wave % GM;
+  const int half = lane >> 5, r32 = lane & 31;
+  const int sw = (r32 >> 1) & 3;
+  // byte offsets of this lane's fragment rows and scales inside a stage
+  const int wrow = wn * 32 * WN + r32, xrow = RW + wm * 32 * WM + r32;
+  const int piece[2] = {((2 * half) ^ sw) * 16, ((2 * half + 1) ^ sw) * 16};
+
+  f32x16 acc[WN][WM];
+#pragma unroll
+  for (int a = 0; a < WN; ++a)
+#pragma unroll
+    for (int b = 0; b < WM; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[a][b][e] = 0.f;
+
+  i32x4 fw[2][WN], fx[2][WM];
+  int sw_[WN], sx_[WM];
+  auto read_frags = [&](int which, int st) {
+    const uint8_t* s = smem + (st & 3) * STAGE + piece[which];
+#pragma unroll
+    for (int a = 0; a < WN; ++a) fw[which][a] = *reinterpret_cast<const i32x4*>(s + (wrow + a * 32) * 64);
+#pragma unroll
+    for (int b = 0; b < WM; ++b) fx[which][b] = *reinterpret_cast<const i32x4*>(s + (xrow + b * 32) * 64);
+  };
+  auto read_scales = [&](int st, int (&tw)[WN], int (&tx)[WM]) {
+    const uint8_t* s = smem + SCALES + ((st >> 2) & 1) * SBUF + (st & 3) * 4 + 2 * half;
+#pragma unroll
+    for (int a = 0; a < WN; ++a) tw[a] = *reinterpret_cast<const uint16_t*>(s + (wrow + a * 32) * 16);
+#pragma unroll
+    for (int b = 0; b < WM; ++b) tx[b] = *reinterpret_cast<const uint16_t*>(s + (xrow + b * 32) * 16);
+  };
+
+  load_scales(0);
+  load_codes(0);
+  for (int st = 1; st < 4 && st < stages; ++st) load_codes(st);
+  if (stages > 3)
+    wait_vm<3 * NC>();
+  else
+    wait_vm<0>();
+  wait_lgkm0();
+  __builtin_amdgcn_s_barrier();
+  read_frags(0, 0);
+  read_scales(0, sw_, sx_);
+
+  for (int st0 = 0; st0 < stages; st0 += 4) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const int st = st0 + d;
+      if (st >= stages) break;
+      read_frags(1, st);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int a = 0; a < WN; ++a)
+#pragma unroll
+        for (int b = 0; b < WM; ++b) acc[a][b] = mfma_mx4_32(fw[0][a], fx[0][b], acc[a][b], sw_[a], sx_[b], 0);
+      __builtin_amdgcn_sched_barrier(0);
+      int nw[WN], nx[WM];
+      if (st + 1 < stages) {
+        // this wave has its fragments of stage st, and its loads of stage
+        // st + 1 (and of the scales that start there) have landed: what was
+        // issued since is the codes of stages st + 2 and st + 3, and at most
+        // some scales (none where all of a wave's lanes copied by words, so
+        // they are not counted)
+        wait_lgkm0();
+        if (st + 3 < stages)
+          wait_vm<2 * NC>();
+        else
+          wait_vm<0>();
+        __builtin_amdgcn_s_barrier();
+        if (d == 0 && st + 4 < stages) load_scales(st / 4 + 1);
+        if (st + 4 < stages) load_codes(st + 4);
+        read_frags(0, st + 1);
+        read_scales(st + 1, nw, nx);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int a = 0; a < WN; ++a)
+#pragma unroll
+        for (int b = 0; b < WM; ++b) acc[a][b] = mfma_mx4_32(fw[1][a], fx[1][b], acc[a][b], sw_[a], sx_[b], 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int a = 0; a < WN; ++a) sw_[a] = nw[a];
+#pragma unroll
+      for (int b = 0; b < WM; ++b) sx_[b] = nx[b];
+    }
+  }
+
+  // Lane l of a 32 x 32 result holds n = 8 (e / 4) + 4 (l / 32) + e % 4 and
+  // m = l % 32.  Each wave turns 32 rows of its part at a time through its own
+  // LDS region and stores whole 16-byte pieces of rows.
+  constexpr int ES = OUT == kF32 ? 4 : 2;
+  constexpr int PITCH = 32 * WN * ES + 16;
+  static_assert(WAVES * 32 * PITCH <= gemm_lds_bytes<RX, RW>(), "epilogue fits the tile's LDS");
+  __builtin_amdgcn_s_barrier();  // every wave is done with the stages
+  uint8_t* mine = smem + wave * 32 * PITCH;
+  const int64_t nw0 = n0 + wn * 32 * WN, mw0 = m0 + wm * 32 * WM;
+#pragma unroll
+  for (int b = 0; b < WM; ++b) {
+#pragma unroll
+    for (int a = 0; a < WN; ++a)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint8_t* p = mine + r32 * PITCH + (a * 32 + q * 8 + half * 4) * ES;
+        const float v0 = acc[a][b][4 * q], v1 = acc[a][b][4 * q + 1], v2 = acc[a][b][4 * q + 2], v3 = acc[a][b][4 * q + 3];
+        if constexpr (OUT == kF32)
+          *reinterpret_cast<f32x4*>(p) = f32x4{v0, v1, v2, v3};
+        else
+          *reinterpret_cast<u32x2*>(p) = u32x2{narrow2<OUT>(v0, v1), narrow2<OUT>(v2, v3)};
+      }
+    wait_lgkm0();  // the region is the wave's own: its LDS accesses stay in order
+    constexpr int PIECES = 32 * WN * ES / 16;  // 16-byte pieces of a row
+    constexpr int PER = 16 / ES;
+#pragma unroll
+    for (int j = 0; j < PIECES / 2; ++j) {
+      const int i = j * 64 + lane;
+      const int r = i / PIECES, c = i - r * PIECES;
+      const int64_t m = mw0 + b * 32 + r, n = nw0 + c * PER;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(mine + r * PITCH + c * 16);
+      if (m < x.rows && n < w.rows) {
+        auto* dst = y + m * stride + n;
+        if (n + PER <= w.rows) {
+          *reinterpret_cast<u32x4_any*>(dst) = v;
+        } else {
+#pragma unroll
+          for (int e = 0; e < PER; ++e)
+            if (n + e < w.rows) {
+              if constexpr (OUT == kF32)
+                dst[e] = __uint_as_float(v[e]);
+              else
+                dst[e] = static_cast<uint16_t>(v[e / 2] >> (16 * (e & 1)));
+            }
+        }
+      }
+    }
+    wait_lgkm0();
+  }
+}
+
+// Few rows of x: y[m][n], m < 32 MT, for 32 rows of W a workgroup.  Every byte
+// of W is used by one wave only, so its fragments come straight from memory;
+// the 8 waves share the summed index, 256 elements (one 128-byte line of a row)
+// a turn, and their sums meet in LDS in a fixed order.  Bound by reading W; x
+// is read by every workgroup, from the L2s.
+template <int OUT, int MT>
+__global__ __launch_bounds__(512) void mx4_skinny_kernel(Mx4Operand x, Mx4Operand w, int64_t ld,
+                                                        typename Elem<OUT>::type* __restrict__ y, int64_t stride) {
+  __shared__ float part[8][16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int half = lane >> 5, r32 = lane & 31;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 32;
+  const int64_t cpitch = ld / 2, spitch = ld / 32;
+  const int64_t wr = n0 + r32 < w.rows ? n0 + r32 : w.rows - 1;
+  const uint8_t* wc = w.codes + wr * cpitch + half * 64;
+  const uint8_t* ws = w.scales + wr * spitch + half * 4;
+  const uint8_t* xc[MT];
+  const uint8_t* xs[MT];
+#pragma unroll
+  for (int b = 0; b < MT; ++b) {
+    const int64_t r = b * 32 + r32 < x.rows ? b * 32 + r32 : x.rows - 1;
+    xc[b] = x.codes + r * cpitch + half * 64;
+    xs[b] = x.scales + r * spitch + half * 4;
+  }
+  f32x16 acc[MT];
+#pragma unroll
+  for (int b = 0; b < MT; ++b)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[b][e] = 0.f;
+
+  for (int64_t k = static_cast<int64_t>(wave) * 256; k < ld; k += 8 * 256) {
+    const bool in = k + half * 128 < ld;  // the last turn may be half a line: zeros for the other
+    i32x4 fw[4], fx[MT][4];
+    int sw = 0, sx[MT];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) fw[i] = in ? *reinterpret_cast<const i32x4*>(wc + k / 2 + i * 16) : i32x4{0, 0, 0, 0};
+    sw = in ? *reinterpret_cast<const int*>(ws + k / 32) : 0;
+#pragma unroll
+    for (int b = 0; b < MT; ++b) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        fx[b][i] = in ? *reinterpret_cast<const i32x4*>(xc[b] + k / 2 + i * 16) : i32x4{0, 0, 0, 0};
+      sx[b] = in ? *reinterpret_cast<const int*>(xs[b] + k / 32) : 0;
+    }
+#pragma unroll
+    for (int b = 0; b < MT; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[b] = mfma_mx4_32(fw[i], fx[b][i], acc[b], sw, sx[b], i);
+  }
+#pragma unroll
+  for (int b = 0; b < MT; ++b) {
+    if (b > 0) __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) part[wave][e][lane] = acc[b][e];
+    __syncthreads();
+    // output o of 1024: row m = o / 32, column n = o % 32
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int o = j * 512 + threadIdx.x;
+      const int n = o & 31, m = o >> 5;
+      const int e = (n >> 3) * 4 + (n & 3), l = ((n >> 2) & 1) * 32 + m;
+      float s = part[0][e][l];
+#pragma unroll
+      for (int v = 1; v < 8; ++v) s += part[v][e][l];
+      if (b * 32 + m < x.rows && n0 + n < w.rows) store1<OUT>(y + (b * 32 + m) * stride + n0 + n, s);
+    }
+  }
+}
+
+typedef float f32x4_acc __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ f32x4_acc mfma_mx4_16(i32x4 a, i32x4 b, f32x4_acc c, int sa, int sb, int which) {
+  const i32x8 a8 = {a.x, a.y, a.z, a.w, 0, 0, 0, 0}, b8 = {b.x, b.y, b.z, b.w, 0, 0, 0, 0};
+  switch (which) {
+    case 0: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, 0, sa, 0, sb);
+    case 1: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, 1, sa, 0, sb);
+    case 2: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, 2, sa, 0, sb);
+    default: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, 3, sa, 0, sb);
+  }
+}
+
+// Up to 16 rows of x, quantised here: y[m][n] for 16 rows of W a workgroup.
+// The 16x16x128 instruction's lane holds a block of 32 elements of one row of
+// x, so a block's max is the lane's own and no second launch is needed.  A
+// turn of a wave is 512 elements: lane group g takes its elements 128 g ...
+// 128 g + 127, 64 contiguous bytes of W's codes and one word of scales.
+template <int TY, int OUT>
+__global__ __launch_bounds__(512) void mx4_decode_kernel(const typename Elem<TY>::type* __restrict__ x, int64_t m, int64_t k,
+                                                        int64_t x_stride, Mx4Operand w, int64_t ld,
+                                                        typename Elem<OUT>::type* __restrict__ y, int64_t stride) {
+  __shared__ float part[8][4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int g = lane >> 4, r16 = lane & 15;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const int64_t wr = n0 + r16 < w.rows ? n0 + r16 : w.rows - 1;
+  const uint8_t* wc = w.codes + wr * (ld / 2) + g * 64;
+  const uint8_t* ws = w.scales + wr * (ld / 32) + g * 4;
+  const auto* xr = x + (r16 < m ? r16 : 0) * x_stride;
+  f32x4_acc acc = {0.f, 0.f, 0.f, 0.f};
+  for (int64_t at = static_cast<int64_t>(wave) * 512; at < ld; at += 8 * 512) {
+    const bool in = at + g * 128 < ld;
+    i32x4 fw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) fw[i] = in ? *reinterpret_cast<const i32x4*>(wc + at / 2 + i * 16) : i32x4{0, 0, 0, 0};
+    const int sw = in ? *reinterpret_cast<const int*>(ws + at / 32) : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      i32x4 fx = {0, 0, 0, 0};
+      uint32_t byte = 1;
+      const int64_t c = at + g * 128 + i * 32;
+      if (r16 < m && c < k) {
+        float v[4][8];
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          load8<TY>(xr, c + j * 8, k, v[j]);
+          top = max_u32(top, amax_bits(v[j]));
+        }
+        byte = scale_byte<kMx4>(top);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) fx[j] = static_cast<int>(encode_mx4(v[j], byte));
+      }
+      acc = mfma_mx4_16(fw[i], fx, acc, sw, static_cast<int>(byte), i);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) part[wave][e][lane] = acc[e];
+  __syncthreads();
+  // lane l of the result holds n = 4 (l / 16) + e and m = l % 16
+  if (threadIdx.x < 256) {
+    const int n = threadIdx.x & 15, row = threadIdx.x >> 4;
+    const int e = n & 3, l = (n >> 2) * 16 + row;
+    float s = part[0][e][l];
+#pragma unroll
+    for (int v = 1; v < 8; ++v) s += part[v][e][l];
+    if (row < m && n0 + n < w.rows) store1<OUT>(y + row * stride + n0 + n, s);
+  }
+}
+
+}  // namespace mx
+}  // namespace casgd

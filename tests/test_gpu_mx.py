@@ -124,6 +124,13 @@ def test_linear(m, k, n):
         assert torch.equal(got, again)  # the same bits, whatever the strides
 
 
+@pytest.mark.parametrize("m,k,n", [(4100, 200, 4099), (3900, 1700, 4200)])
+def test_linear_of_many_tiles(m, k, n):
+    w, x = stored(values((n, k), 7) / np.sqrt(k), "mx4"), cuda(values((m, k), 8, 0.5), "bf16")
+    wv = H.dequantize(w.codes.cpu().numpy(), w.scales.cpu().numpy(), k, "mx4")
+    close(B.mx4_linear(x, w), H.rounded(host(x), "mx4"), wv.T, "bf16")
+
+
 def test_linear_propagates_nan_blocks():
     x, w = values((3, 256), 1), values((40, 256), 2)
     x[1, 200], w[7, 3], w[9, 255] = np.inf, np.nan, -np.inf
