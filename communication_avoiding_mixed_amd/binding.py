@@ -63,8 +63,9 @@ SIGNATURES = {
     "casgd_mx_dequantize": (_I, [_VP, _VP, _I, _I64, _I64, _VP, _I, _I64, _VP]),
     "casgd_mx4_linear_workspace": (_I64, [_I64, _I64, _I64]),
     "casgd_mx4_linear": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _VP, _I64, _VP, _I, _I64, _VP, _I64, _VP]),
-    "casgd_mx4_grad_input": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _VP, _I64, _VP, _I, _I64, _VP]),
-    "casgd_mx8_grad_weight": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _VP, _I64, _VP, _I, _I64, _I, _VP]),
+    "casgd_mx_grad_workspace": (_I64, [_I, _I64, _I64, _I64, _VP, _I, _I64]),
+    "casgd_mx4_grad_input": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _VP, _I64, _VP, _I, _I64, _VP, _I64, _VP]),
+    "casgd_mx8_grad_weight": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _VP, _I64, _VP, _I, _I64, _I, _VP, _I64, _VP]),
     "casgd_token_logps": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _VP, _VP]),
     "casgd_pref_workspace": (_I64, [_I64]),
     "casgd_pref_loss": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _VP, _I64, _VP, _I, _F, _F, _I, _VP, _VP, _VP, _VP, _VP,
@@ -440,8 +441,10 @@ def mx4_grad_input(dy, w: MXMatrix, out_dtype=None):
     out_dtype = out_dtype or dy.dtype
     out_ty = _type_id(out_dtype, "out_dtype")
     dx = torch.empty((m, w.cols), dtype=out_dtype, device=device)
+    need = load().casgd_mx_grad_workspace(0, m, n, w.cols, dy.data_ptr(), ty, stride)
+    ws = torch.empty(max(need, 0), dtype=torch.uint8, device=device)
     _call(device, "casgd_mx4_grad_input", dy.data_ptr(), ty, m, n, stride, w.codes.data_ptr(), w.scales.data_ptr(),
-          w.cols, dx.data_ptr(), out_ty, w.cols)
+          w.cols, dx.data_ptr(), out_ty, w.cols, ws.data_ptr(), need)
     return dx
 
 
@@ -466,8 +469,10 @@ def mx8_grad_weight(dy, x: MXMatrix, out=None, accumulate: bool = False, out_dty
     out_ty, rows, cols, out_stride = _rows_of(out, "out")
     if (rows, cols) != (n, x.cols) or out.device != device:
         raise ValueError(f"out must be {n} x {x.cols} on {device}")
+    need = load().casgd_mx_grad_workspace(1, t, n, x.cols, dy.data_ptr(), ty, stride)
+    ws = torch.empty(max(need, 0), dtype=torch.uint8, device=device)
     _call(device, "casgd_mx8_grad_weight", dy.data_ptr(), ty, t, n, stride, x.codes.data_ptr(), x.scales.data_ptr(),
-          x.cols, out.data_ptr(), out_ty, out_stride, 1 if accumulate else 0)
+          x.cols, out.data_ptr(), out_ty, out_stride, 1 if accumulate else 0, ws.data_ptr(), need)
     return out
 
 

@@ -62,6 +62,76 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t tiles_m, uint32_t 
   bn = in / rows;
 }
 
+// A wave's results to rows row0 ... and columns col0 ... of out.  Lane l of a
+// 32 x 32 result holds columns 8 (e / 4) + 4 (l / 32) + e % 4 of row l % 32; 32
+// rows at a time go through the wave's own LDS region `mine`, 32 rows of
+// 32 WN elements and 16 bytes, to whole 16-byte pieces of rows.
+template <int OUT, int WM, int WN>
+__device__ __forceinline__ void store_tile(const f32x16 (&acc)[WN][WM], uint8_t* mine, typename Elem<OUT>::type* out,
+                                           int64_t stride, int64_t row0, int64_t col0, int64_t rows, int64_t cols,
+                                           int accumulate) {
+  constexpr int ES = OUT == kF32 ? 4 : 2;
+  constexpr int PITCH = 32 * WN * ES + 16;
+  constexpr int PIECES = 32 * WN * ES / 16;  // 16-byte pieces of a row
+  constexpr int PER = 16 / ES;
+  const int lane = threadIdx.x & 63, half = lane >> 5, r32 = lane & 31;
+#pragma unroll
+  for (int b = 0; b < WM; ++b) {
+#pragma unroll
+    for (int a = 0; a < WN; ++a)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint8_t* p = mine + r32 * PITCH + (a * 32 + q * 8 + half * 4) * ES;
+        const float v0 = acc[a][b][4 * q], v1 = acc[a][b][4 * q + 1], v2 = acc[a][b][4 * q + 2], v3 = acc[a][b][4 * q + 3];
+        if (OUT == kF32 || accumulate) {
+          // sums to be added to are rounded once, after the addition
+          if constexpr (OUT == kF32) *reinterpret_cast<f32x4*>(p) = f32x4{v0, v1, v2, v3};
+          else {
+            auto* o = out + (row0 + b * 32 + r32) * stride + col0 + a * 32 + q * 8 + half * 4;
+            const float v[4] = {v0, v1, v2, v3};
+            if (row0 + b * 32 + r32 < rows)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (col0 + a * 32 + q * 8 + half * 4 + e < cols) store1<OUT>(o + e, load1<OUT>(o + e) + v[e]);
+          }
+        } else if constexpr (OUT != kF32) {
+          *reinterpret_cast<u32x2*>(p) = u32x2{narrow2<OUT>(v0, v1), narrow2<OUT>(v2, v3)};
+        }
+      }
+    if (OUT != kF32 && accumulate) continue;
+    wait_lgkm0();  // the region is the wave's own: its LDS accesses stay in order
+#pragma unroll
+    for (int j = 0; j < PIECES / 2; ++j) {
+      const int i = j * 64 + lane;
+      const int r = i / PIECES, c = i - r * PIECES;
+      const int64_t m = row0 + b * 32 + r, n = col0 + c * PER;
+      u32x4 v = *reinterpret_cast<const u32x4*>(mine + r * PITCH + c * 16);
+      if (m < rows && n < cols) {
+        auto* dst = out + m * stride + n;
+        if (n + PER <= cols) {
+          if constexpr (OUT == kF32)
+            if (accumulate) {
+              const u32x4 old = *reinterpret_cast<const u32x4_any*>(dst);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(old[e]));
+            }
+          *reinterpret_cast<u32x4_any*>(dst) = v;
+        } else {
+#pragma unroll
+          for (int e = 0; e < PER; ++e)
+            if (n + e < cols) {
+              if constexpr (OUT == kF32)
+                dst[e] = accumulate ? dst[e] + __uint_as_float(v[e]) : __uint_as_float(v[e]);
+              else
+                dst[e] = static_cast<uint16_t>(v[e / 2] >> (16 * (e & 1)));
+            }
+        }
+      }
+    }
+    wait_lgkm0();
+  }
+}
+
 struct Mx4Operand {
   const uint8_t* codes;
   const uint8_t* scales;
@@ -249,55 +319,10 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void mx4_gemm_kernel(Mx4Operand x,
     }
   }
 
-  // Lane l of a 32 x 32 result holds n = 8 (e / 4) + 4 (l / 32) + e % 4 and
-  // m = l % 32.  Each wave turns 32 rows of its part at a time through its own
-  // LDS region and stores whole 16-byte pieces of rows.
-  constexpr int ES = OUT == kF32 ? 4 : 2;
-  constexpr int PITCH = 32 * WN * ES + 16;
+  constexpr int PITCH = 32 * WN * (OUT == kF32 ? 4 : 2) + 16;
   static_assert(WAVES * 32 * PITCH <= gemm_lds_bytes<RX, RW>(), "epilogue fits the tile's LDS");
   __builtin_amdgcn_s_barrier();  // every wave is done with the stages
-  uint8_t* mine = smem + wave * 32 * PITCH;
-  const int64_t nw0 = n0 + wn * 32 * WN, mw0 = m0 + wm * 32 * WM;
-#pragma unroll
-  for (int b = 0; b < WM; ++b) {
-#pragma unroll
-    for (int a = 0; a < WN; ++a)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint8_t* p = mine + r32 * PITCH + (a * 32 + q * 8 + half * 4) * ES;
-        const float v0 = acc[a][b][4 * q], v1 = acc[a][b][4 * q + 1], v2 = acc[a][b][4 * q + 2], v3 = acc[a][b][4 * q + 3];
-        if constexpr (OUT == kF32)
-          *reinterpret_cast<f32x4*>(p) = f32x4{v0, v1, v2, v3};
-        else
-          *reinterpret_cast<u32x2*>(p) = u32x2{narrow2<OUT>(v0, v1), narrow2<OUT>(v2, v3)};
-      }
-    wait_lgkm0();  // the region is the wave's own: its LDS accesses stay in order
-    constexpr int PIECES = 32 * WN * ES / 16;  // 16-byte pieces of a row
-    constexpr int PER = 16 / ES;
-#pragma unroll
-    for (int j = 0; j < PIECES / 2; ++j) {
-      const int i = j * 64 + lane;
-      const int r = i / PIECES, c = i - r * PIECES;
-      const int64_t m = mw0 + b * 32 + r, n = nw0 + c * PER;
-      const u32x4 v = *reinterpret_cast<const u32x4*>(mine + r * PITCH + c * 16);
-      if (m < x.rows && n < w.rows) {
-        auto* dst = y + m * stride + n;
-        if (n + PER <= w.rows) {
-          *reinterpret_cast<u32x4_any*>(dst) = v;
-        } else {
-#pragma unroll
-          for (int e = 0; e < PER; ++e)
-            if (n + e < w.rows) {
-              if constexpr (OUT == kF32)
-                dst[e] = __uint_as_float(v[e]);
-              else
-                dst[e] = static_cast<uint16_t>(v[e / 2] >> (16 * (e & 1)));
-            }
-        }
-      }
-    }
-    wait_lgkm0();
-  }
+  store_tile<OUT, WM, WN>(acc, smem + wave * 32 * PITCH, y, stride, m0 + wm * 32 * WM, n0 + wn * 32 * WN, x.rows, w.rows, 0);
 }
 
 // Few rows of x: y[m][n], m < 32 MT, for 32 rows of W a workgroup.  Every byte

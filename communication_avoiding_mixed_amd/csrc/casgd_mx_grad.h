@@ -1,0 +1,239 @@
+// Gradients of the low-precision layer on bf16 matrix instructions:
+//
+//   out[i][j] = sum_t X(t, i) C[t][j]
+//
+// C is the coded matrix widened to bf16 (its values are exact there), its
+// rows the summed index.  X is the gradient dy: rows of the summed index for
+// the weight gradient (ACROSS), rows of the output for the input gradient.  A
+// gradient of more than 8 significant bits comes as a sum of bf16 parts (two
+// for fp16, three for float32, both exact), laid one after another along the
+// summed index; C is walked again for each part.
+#pragma once
+
+#include "casgd_mx_gemm.h"
+
+namespace casgd {
+namespace mx {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+struct GradArgs {
+  const uint16_t* x;  // dy as bf16 (or its parts)
+  int64_t x_stride;   // elements
+  int64_t x_part;     // elements from one part to the next
+  int64_t rows;       // of the output
+  const uint16_t* c;  // [stages * 32][ld]
+  int64_t ld;
+  int64_t cols;       // of the output
+  int64_t depth;      // summed index
+  int stages;         // per part: depth / 32, rounded up
+  int parts;
+  int whole;          // X holds zeros up to stages * 32 (a copy), so no stage is ragged
+  uint32_t tiles_m, tiles_n, band;
+  int per_split;      // stages of one split of the summed index
+};
+
+// the ring, or the epilogue's regions of float32 rows if they are larger
+template <int RX, int RC, int GM, int GN>
+constexpr int grad_lds_bytes() {
+  constexpr int ring = 4 * (RX + RC) * 64, regions = GM * GN * 32 * (RC / GN * 4 + 16);
+  return ring > regions ? ring : regions;
+}
+
+// One RX x RC tile of the output by GM x GN waves, 32 of the summed index a
+// stage, four stages in a ring of LDS filled three ahead by direct-to-LDS
+// loads.
+//
+// A matrix whose rows are the summed index is staged as it lies, 32 rows of
+// the tile's columns, and transposed by the LDS read (ds_read_b64_tr_b16: 16
+// lanes read four rows of 16 columns, a lane gets its column's four values).
+// Those four rows' 32 bytes would meet in the same banks, so row t's 16-byte
+// pieces are stored at piece XOR 2 (t mod 4).  A matrix whose rows are the
+// output is staged as 64 bytes of each row, as the 4-bit product's codes are.
+template <int OUT, bool ACROSS, int RX, int RC, int GM, int GN>
+__global__ __launch_bounds__(64 * GM * GN, 2) void mx_grad_kernel(GradArgs g, typename Elem<OUT>::type* __restrict__ out_,
+                                                                 int64_t stride, int64_t split_stride, int accumulate) {
+  constexpr int WM = RX / GM / 32, WC = RC / GN / 32, WAVES = GM * GN;
+  constexpr int STAGE = (RX + RC) * 64, XBASE = RC * 64;
+  constexpr int NC = (RX + RC) / 16 / WAVES;  // 1 KB loads of a wave per stage
+  static_assert((RX + RC) % (16 * WAVES) == 0, "whole loads");
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint32_t bm, bn;
+  tile_of(blockIdx.x, g.tiles_m, g.tiles_n, g.band, bm, bn);
+  const int64_t i0 = static_cast<int64_t>(bm) * RX, j0 = static_cast<int64_t>(bn) * RC;
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)smem));
+  const int first = static_cast<int>(blockIdx.y) * g.per_split;
+  const int last = first + g.per_split < g.stages * g.parts ? first + g.per_split : g.stages * g.parts;
+  const int stages = last - first;
+
+  // this lane's piece of each of the wave's loads, in bytes from the operand's
+  // stage pointer; columns past the matrix read the tile's first piece and
+  // rows past it the last row, which only feed outputs that are not stored
+  uint32_t off[NC];
+  int row_in[NC], piece_in[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int load = wave * NC + i;
+    const bool is_c = load < RC / 16;
+    const int l = is_c ? load : load - RC / 16;
+    if (is_c || ACROSS) {
+      const int per_row = is_c ? RC / 8 : RX / 8;
+      const int slot = l * 64 + lane;
+      const int t = slot / per_row;
+      int p = (slot - t * per_row) ^ ((t & 3) << 1);
+      row_in[i] = t;
+      piece_in[i] = p;
+      const int64_t width = is_c ? g.ld - j0 : g.rows - i0;
+      if (p * 8 >= width) p = 0;
+      off[i] = static_cast<uint32_t>(t * (is_c ? g.ld : g.x_stride) * 2) + p * 16;
+    } else {
+      int r = l * 16 + (lane >> 2);
+      const int p = (lane & 3) ^ ((r >> 1) & 3);
+      if (r >= g.rows - i0) r = static_cast<int>(g.rows - i0) - 1;
+      row_in[i] = r;
+      piece_in[i] = p;
+      off[i] = static_cast<uint32_t>(r * g.x_stride * 2) + p * 16;
+    }
+  }
+  // stage pointers of the next load: inside a part one step each, then the
+  // next part of X and C from its start
+  const int64_t xstep = ACROSS ? 32 * g.x_stride : 32, cstep = 32 * g.ld;
+  int lpart = first / g.stages, lst = first - lpart * g.stages;
+  const uint16_t* xp = g.x + lpart * g.x_part + lst * xstep + (ACROSS ? i0 : i0 * g.x_stride);
+  const uint16_t* cp = g.c + lst * cstep + j0;
+  auto load_stage = [&](int slot) {
+    const bool ragged = !g.whole && lst == g.stages - 1;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int load = wave * NC + i;
+      const bool is_c = load < RC / 16;
+      const uint32_t to = slot * STAGE + load * 1024;
+      if (is_c || !ragged) {
+        load_lds16(lds0 + to, is_c ? cp : xp, off[i]);
+        continue;
+      }
+      // X's last stage: elements past the summed index are zeros, and nothing
+      // past the matrix is read
+      const int64_t t0 = static_cast<int64_t>(lst) * 32;
+      int valid;  // elements of this piece
+      if (ACROSS) {
+        const int64_t left = g.rows - i0 - piece_in[i] * 8;
+        valid = t0 + row_in[i] < g.depth ? (left < 8 ? static_cast<int>(left < 0 ? 0 : left) : 8) : 0;
+      } else {
+        const int64_t left = g.depth - t0 - piece_in[i] * 8;
+        valid = left < 8 ? static_cast<int>(left < 0 ? 0 : left) : 8;
+      }
+      if (valid == 8) {
+        load_lds16(lds0 + to, xp, off[i]);
+      } else {
+        const uint16_t* src = reinterpret_cast<const uint16_t*>(reinterpret_cast<const uint8_t*>(xp) + off[i]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          *reinterpret_cast<uint16_t*>(smem + to + lane * 16 + e * 2) = e < valid ? src[e] : uint16_t{0};
+      }
+    }
+    xp += xstep;
+    cp += cstep;
+    if (++lst == g.stages) {
+      lst = 0;
+      xp += g.x_part - g.stages * xstep;
+      cp -= g.stages * cstep;
+    }
+  };
+
+  const int wn = wave / GM, wm = wave % GM;
+  const int half = lane >> 5, r32 = lane & 31;
+  // transposed read: row (lane % 16) / 4 of four, columns 16 (lane / 16 % 2) + 4 (lane % 4)
+  const int trow = 8 * half + ((lane & 15) >> 2);
+  const int tlow = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1), tx = ((lane & 15) >> 2) << 1;
+  const int tbyte = (lane & 1) * 8;
+  const int teven = (tlow ^ tx) * 16 + tbyte, todd = ((4 + tlow) ^ tx) * 16 + tbyte;
+  const int sw = (r32 >> 1) & 3;
+
+  // tile `a` (32 columns from column 32 a) of a staged matrix `width` columns wide
+  auto read_across = [&](const uint8_t* s, int width, int a, int which) -> bf16x8 {
+    const uint8_t* p = s + (which * 16 + trow) * width * 2 + (a >> 1) * 128 + ((a & 1) ? todd : teven);
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * width * 2));
+    const __attribute__((ext_vector_type(8))) short v = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    return __builtin_bit_cast(bf16x8, v);
+  };
+
+  f32x16 acc[WC][WM];
+#pragma unroll
+  for (int a = 0; a < WC; ++a)
+#pragma unroll
+    for (int b = 0; b < WM; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[a][b][e] = 0.f;
+
+  bf16x8 fc[2][WC], fx[2][WM];
+  auto read_frags = [&](int which, int st) {
+    const uint8_t* s = smem + (st & 3) * STAGE;
+#pragma unroll
+    for (int a = 0; a < WC; ++a) fc[which][a] = read_across(s, RC, wn * WC + a, which);
+#pragma unroll
+    for (int b = 0; b < WM; ++b) {
+      if constexpr (ACROSS)
+        fx[which][b] = read_across(s + XBASE, RX, wm * WM + b, which);
+      else
+        fx[which][b] = *reinterpret_cast<const bf16x8*>(s + XBASE + ((wm * WM + b) * 32 + r32) * 64 +
+                                                       (((2 * which + half) ^ sw) * 16));
+    }
+  };
+
+  for (int st = 0; st < 4 && st < stages; ++st) load_stage(st);
+  // a ragged stage may have fewer loads, so it is never among those counted
+  if (stages > 4)
+    wait_vm<3 * NC>();
+  else
+    wait_vm<0>();
+  wait_lgkm0();
+  __builtin_amdgcn_s_barrier();
+  read_frags(0, 0);
+
+  for (int st0 = 0; st0 < stages; st0 += 4) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const int st = st0 + d;
+      if (st >= stages) break;
+      read_frags(1, st);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int a = 0; a < WC; ++a)
+#pragma unroll
+        for (int b = 0; b < WM; ++b) acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fc[0][a], fx[0][b], acc[a][b], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      if (st + 1 < stages) {
+        // this wave has its fragments of stage st, and its loads of stage
+        // st + 1 have landed: stages st + 2 and st + 3 may be on their way
+        wait_lgkm0();
+        if (st + 4 < stages)
+          wait_vm<2 * NC>();
+        else
+          wait_vm<0>();
+        __builtin_amdgcn_s_barrier();
+        if (st + 4 < stages) load_stage(st & 3);
+        read_frags(0, st + 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int a = 0; a < WC; ++a)
+#pragma unroll
+        for (int b = 0; b < WM; ++b) acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fc[1][a], fx[1][b], acc[a][b], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+
+  __builtin_amdgcn_s_barrier();  // every wave is done with the stages
+  constexpr int PITCH = 32 * WC * (OUT == kF32 ? 4 : 2) + 16;
+  store_tile<OUT, WM, WC>(acc, smem + wave * 32 * PITCH, out_ + static_cast<int64_t>(blockIdx.y) * split_stride, stride,
+                          i0 + wm * 32 * WM, j0 + wn * 32 * WC, g.rows, g.cols, accumulate);
+}
+
+}  // namespace mx
+}  // namespace casgd

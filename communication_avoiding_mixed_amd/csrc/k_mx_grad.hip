@@ -1,0 +1,309 @@
+// Backward pass of the low-precision layer with its C entry points:
+//
+//   grad input   dx[m][k] = sum_n dy[m][n] W4[n][k]
+//   grad weight  dW[n][k] = sum_t dy[t][n] X8[t][k]
+//
+// The coded matrix is widened to bf16 once into the workspace (exact), and a
+// gradient that is no bf16 matrix with 16-byte aligned rows is copied there,
+// fp16 and float32 ones as two and three bf16 parts that sum to it exactly.
+#include "casgd.h"
+#include "casgd_internal.h"
+#include "casgd_mx_grad.h"
+
+namespace casgd {
+namespace mx {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Rows of codes to bf16, [rows_pad][ld], zeros in rows past the matrix.
+template <int FMT>
+__global__ __launch_bounds__(kThreads) void mx_widen_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+                                                           int64_t chunks, int64_t chunks_pad, uint16_t* __restrict__ out) {
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
+  for (int64_t at = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; at < chunks_pad; at += step) {
+    u32x4 r = {0u, 0u, 0u, 0u};
+    if (at < chunks) {
+      const float scale = scale_value(scales[at >> 2]);
+      float v[8];
+      if constexpr (FMT == kMx4)
+        decode_mx4(reinterpret_cast<const uint32_t*>(codes)[at], scale, v);
+      else
+        decode_mx8(reinterpret_cast<const u32x2*>(codes)[at], scale, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = narrow2<kBF16>(v[2 * i], v[2 * i + 1]);
+    }
+    reinterpret_cast<u32x4*>(out)[at] = r;
+  }
+}
+
+// dy (rows x cols) as PARTS bf16 matrices [rows_pad][pitch], zeros in the
+// padding.  Each part keeps the 8 leading bits of what is left, cut towards
+// zero so that no part overflows; a value that is not finite is its first part.
+template <int TY, int PARTS>
+__global__ __launch_bounds__(kThreads) void split_kernel(const typename Elem<TY>::type* __restrict__ dy, int64_t rows,
+                                                        int64_t cols, int64_t stride, int64_t rows_pad, int64_t pitch,
+                                                        uint16_t* __restrict__ out) {
+  const int64_t per_row = pitch / 8, chunks = rows_pad * per_row;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
+  for (int64_t at = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; at < chunks; at += step) {
+    const int64_t r = at / per_row, c = (at - r * per_row) * 8;
+    float v[8] = {};
+    if (r < rows) load8<TY>(dy + r * stride, c, cols, v);
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) {
+      u32x4 w;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t bits = __float_as_uint(v[i]);
+        const bool fine = (bits & 0x7F800000u) != 0x7F800000u;
+        // a NaN keeps a set fraction bit among the 7 that stay
+        const uint32_t top = fine ? bits >> 16 : (bits >> 16) | ((bits & 0x7FFFFFu) ? 0x40u : 0u);
+        if (i & 1)
+          w[i / 2] |= top << 16;
+        else
+          w[i / 2] = top;
+        v[i] = fine ? v[i] - __uint_as_float(bits & 0xFFFF0000u) : 0.f;
+      }
+      reinterpret_cast<u32x4*>(out)[p * chunks + at] = w;
+    }
+  }
+}
+
+// The splits' float32 sums, added in order, to the output.
+template <int OUT>
+__global__ __launch_bounds__(kThreads) void join_kernel(const float* __restrict__ sums, int splits, int64_t rows, int64_t cols,
+                                                       typename Elem<OUT>::type* __restrict__ out, int64_t stride,
+                                                       int accumulate) {
+  const int64_t count = rows * cols;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
+  for (int64_t at = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; at < count; at += step) {
+    float s = sums[at];
+    for (int i = 1; i < splits; ++i) s += sums[i * count + at];
+    const int64_t r = at / cols;
+    auto* p = out + r * stride + (at - r * cols);
+    store1<OUT>(p, accumulate ? load1<OUT>(p) + s : s);
+  }
+}
+
+template <typename E>
+__global__ __launch_bounds__(kThreads) void zero_kernel(E* __restrict__ out, int64_t rows, int64_t cols, int64_t stride) {
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
+  for (int64_t at = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; at < rows * cols; at += step) {
+    const int64_t r = at / cols;
+    out[r * stride + (at - r * cols)] = E{0};
+  }
+}
+
+unsigned grid_of(int64_t items) {
+  const int64_t g = (items + kThreads - 1) / kThreads;
+  return static_cast<unsigned>(g < 1 ? 1 : g > 256 * 64 ? 256 * 64 : g);
+}
+
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+int parts_of(int type) { return type == kBF16 ? 1 : type == kF16 ? 2 : 3; }
+
+// What a gradient call does, from its sizes, type and alignment.
+struct Plan {
+  int64_t depth, rows, cols, ld;  // out (rows x cols) = sum over depth
+  int64_t x_rows, x_cols;         // dy as it lies
+  bool across;
+  int parts, stages, splits, per_split, tile;
+  bool copy;
+  int64_t pitch, x_pad;  // of the copy
+  int64_t c_bytes, x_bytes, s_bytes;
+};
+
+Plan plan_of(bool across, int64_t m, int64_t n, int64_t k, int type, const void* dy, int64_t stride) {
+  Plan p;
+  p.across = across;
+  p.depth = across ? m : n;
+  p.rows = across ? n : m;
+  p.cols = k;
+  p.ld = ld_of(k);
+  p.x_rows = m;
+  p.x_cols = n;
+  p.parts = parts_of(type);
+  p.stages = static_cast<int>((p.depth + 31) / 32);
+  p.copy = type != kBF16 || reinterpret_cast<uintptr_t>(dy) % 16 != 0 || stride % 8 != 0 || stride > (int64_t{1} << 22);
+  p.pitch = up(n, 32);
+  p.x_pad = across ? up(m, 32) : m;
+  p.c_bytes = up(static_cast<int64_t>(p.stages) * 32 * p.ld * 2, 256);
+  p.x_bytes = p.copy ? up(p.parts * p.x_pad * p.pitch * 2, 256) : 0;
+  // 256 x 256 tiles where there are enough for most of the 256 CUs; with
+  // fewer 128 x 128 tiles than CUs the summed index is split, as long as a
+  // split keeps 8 stages
+  const int64_t big = ((p.rows + 255) / 256) * ((p.cols + 255) / 256);
+  p.tile = big >= 192 ? 256 : 128;
+  const int64_t tiles = ((p.rows + p.tile - 1) / p.tile) * ((p.cols + p.tile - 1) / p.tile);
+  const int64_t total = static_cast<int64_t>(p.stages) * p.parts;
+  int64_t splits = 256 / (tiles < 1 ? 1 : tiles);
+  if (splits > total / 8) splits = total / 8;
+  if (splits < 1) splits = 1;
+  p.per_split = static_cast<int>((total + splits - 1) / splits);
+  p.splits = p.per_split > 0 ? static_cast<int>((total + p.per_split - 1) / p.per_split) : 1;
+  p.s_bytes = p.splits > 1 ? up(p.splits * p.rows * p.cols * 4, 256) : 0;
+  return p;
+}
+
+template <int OUT, bool ACROSS, int RX, int RC, int GM, int GN>
+hipError_t grad_tile_as(const GradArgs& in, int splits, void* out, int64_t stride, int64_t split_stride, int accumulate,
+                        hipStream_t stream) {
+  constexpr int lds = grad_lds_bytes<RX, RC, GM, GN>();
+  auto* kernel = mx_grad_kernel<OUT, ACROSS, RX, RC, GM, GN>;
+  static const hipError_t allowed =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (allowed != hipSuccess) return allowed;
+  GradArgs g = in;
+  const int64_t tm = (g.rows + RX - 1) / RX, tn = (g.cols + RC - 1) / RC;
+  if (tm * tn > (int64_t{1} << 22)) return hipErrorInvalidValue;
+  g.tiles_m = static_cast<uint32_t>(tm);
+  g.tiles_n = static_cast<uint32_t>(tn);
+  g.band = 8;
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(tm * tn), splits), dim3(64 * GM * GN), lds, stream, g,
+                     static_cast<typename Elem<OUT>::type*>(out), stride, split_stride, accumulate);
+  return hipGetLastError();
+}
+
+template <int OUT, bool ACROSS>
+hipError_t grad_as(const GradArgs& g, const Plan& p, void* out, int64_t stride, int64_t split_stride, int accumulate,
+                   hipStream_t stream) {
+  if (p.tile == 256) return grad_tile_as<OUT, ACROSS, 256, 256, 4, 2>(g, p.splits, out, stride, split_stride, accumulate, stream);
+  return grad_tile_as<OUT, ACROSS, 128, 128, 2, 2>(g, p.splits, out, stride, split_stride, accumulate, stream);
+}
+
+template <bool ACROSS>
+hipError_t grad_to(int type, const GradArgs& g, const Plan& p, void* out, int64_t stride, float* sums, int accumulate,
+                   hipStream_t stream) {
+  if (p.splits > 1) {
+    hipError_t e = grad_as<kF32, ACROSS>(g, p, sums, p.cols, p.rows * p.cols, 0, stream);
+    if (e != hipSuccess) return e;
+    const unsigned grid = grid_of(p.rows * p.cols);
+    if (type == kBF16)
+      hipLaunchKernelGGL((join_kernel<kBF16>), dim3(grid), dim3(kThreads), 0, stream, sums, p.splits, p.rows, p.cols,
+                         static_cast<uint16_t*>(out), stride, accumulate);
+    else if (type == kF16)
+      hipLaunchKernelGGL((join_kernel<kF16>), dim3(grid), dim3(kThreads), 0, stream, sums, p.splits, p.rows, p.cols,
+                         static_cast<uint16_t*>(out), stride, accumulate);
+    else
+      hipLaunchKernelGGL((join_kernel<kF32>), dim3(grid), dim3(kThreads), 0, stream, sums, p.splits, p.rows, p.cols,
+                         static_cast<float*>(out), stride, accumulate);
+    return hipGetLastError();
+  }
+  if (type == kBF16) return grad_as<kBF16, ACROSS>(g, p, out, stride, 0, accumulate, stream);
+  if (type == kF16) return grad_as<kF16, ACROSS>(g, p, out, stride, 0, accumulate, stream);
+  return grad_as<kF32, ACROSS>(g, p, out, stride, 0, accumulate, stream);
+}
+
+template <bool ACROSS, int FMT>
+hipError_t run_grad(const Plan& p, const void* dy, int type, int64_t dy_stride, const uint8_t* codes, const uint8_t* scales,
+                    void* out, int out_type, int64_t stride, int accumulate, uint8_t* workspace, hipStream_t stream) {
+  uint16_t* c = reinterpret_cast<uint16_t*>(workspace);
+  uint16_t* x = reinterpret_cast<uint16_t*>(workspace + p.c_bytes);
+  float* sums = reinterpret_cast<float*>(workspace + p.c_bytes + p.x_bytes);
+  const int64_t chunks = p.depth * p.ld / 8, chunks_pad = static_cast<int64_t>(p.stages) * 32 * p.ld / 8;
+  hipLaunchKernelGGL((mx_widen_kernel<FMT>), dim3(grid_of(chunks_pad)), dim3(kThreads), 0, stream, codes, scales, chunks,
+                     chunks_pad, c);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  GradArgs g = {};
+  g.x = static_cast<const uint16_t*>(dy);
+  g.x_stride = dy_stride;
+  if (p.copy) {
+    const unsigned grid = grid_of(p.x_pad * p.pitch / 8);
+    if (type == kBF16)
+      hipLaunchKernelGGL((split_kernel<kBF16, 1>), dim3(grid), dim3(kThreads), 0, stream, static_cast<const uint16_t*>(dy),
+                         p.x_rows, p.x_cols, dy_stride, p.x_pad, p.pitch, x);
+    else if (type == kF16)
+      hipLaunchKernelGGL((split_kernel<kF16, 2>), dim3(grid), dim3(kThreads), 0, stream, static_cast<const uint16_t*>(dy),
+                         p.x_rows, p.x_cols, dy_stride, p.x_pad, p.pitch, x);
+    else
+      hipLaunchKernelGGL((split_kernel<kF32, 3>), dim3(grid), dim3(kThreads), 0, stream, static_cast<const float*>(dy),
+                         p.x_rows, p.x_cols, dy_stride, p.x_pad, p.pitch, x);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    g.x = x;
+    g.x_stride = p.pitch;
+    g.x_part = p.x_pad * p.pitch;
+    g.whole = 1;
+  }
+  g.rows = p.rows;
+  g.c = c;
+  g.ld = p.ld;
+  g.cols = p.cols;
+  g.depth = p.depth;
+  g.stages = p.stages;
+  g.parts = p.parts;
+  g.per_split = p.per_split;
+  return grad_to<ACROSS>(out_type, g, p, out, stride, sums, accumulate, stream);
+}
+
+// sizes whose byte offsets inside a stage stay below 2^32
+constexpr int64_t kMaxGradDim = int64_t{1} << 22;
+
+const char* bad_grad(int64_t m, int64_t n, int64_t k) {
+  if (n > kMaxGradDim || k > kMaxGradDim) return "n and k must be at most 2^22";
+  if (m > (int64_t{1} << 28)) return "too many rows";
+  return nullptr;
+}
+
+}  // namespace
+}  // namespace mx
+}  // namespace casgd
+
+using namespace casgd;
+
+extern "C" {
+
+int64_t casgd_mx_grad_workspace(int weight, int64_t m, int64_t n, int64_t k, const void* dy, int dy_type, int64_t dy_stride) {
+  if (mx::bad_matrix(m, n, dy_stride, dy_type) || k < 1 || mx::bad_grad(m, n, k)) return -1;
+  const mx::Plan p = mx::plan_of(weight != 0, m, n, k, dy_type, dy, dy_stride);
+  return p.c_bytes + p.x_bytes + p.s_bytes;
+}
+
+int casgd_mx4_grad_input(const void* dy, int dy_type, int64_t m, int64_t n, int64_t dy_stride, const uint8_t* w_codes,
+                         const uint8_t* w_scales, int64_t k, void* dx, int dx_type, int64_t dx_stride, void* workspace,
+                         int64_t workspace_bytes, void* hip_stream) {
+  if (const char* why = mx::bad_matrix(m, n, dy_stride, dy_type)) return api_fail(CASGD_EINVAL, why);
+  if (const char* why = mx::bad_matrix(m, k, dx_stride, dx_type)) return api_fail(CASGD_EINVAL, why);
+  if (const char* why = mx::bad_codes(w_codes, w_scales, n, mx::kMx4)) return api_fail(CASGD_EINVAL, why);
+  if (const char* why = mx::bad_grad(m, n, k)) return api_fail(CASGD_EINVAL, why);
+  if (m == 0) return CASGD_OK;
+  if (!dy || !dx || !workspace) return api_fail(CASGD_EINVAL, "NULL pointer");
+  const mx::Plan p = mx::plan_of(false, m, n, k, dy_type, dy, dy_stride);
+  if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return api_fail(CASGD_EINVAL, "workspace must be 256-byte aligned");
+  if (workspace_bytes < p.c_bytes + p.x_bytes + p.s_bytes) return api_fail(CASGD_EINVAL, "workspace too small");
+  const hipError_t e = mx::run_grad<false, mx::kMx4>(p, dy, dy_type, dy_stride, w_codes, w_scales, dx, dx_type, dx_stride, 0,
+                                                     static_cast<uint8_t*>(workspace), static_cast<hipStream_t>(hip_stream));
+  return e == hipSuccess ? CASGD_OK : api_hip_fail(e, "input gradient launch");
+}
+
+int casgd_mx8_grad_weight(const void* dy, int dy_type, int64_t t, int64_t n, int64_t dy_stride, const uint8_t* x_codes,
+                          const uint8_t* x_scales, int64_t k, void* dw, int dw_type, int64_t dw_stride, int accumulate,
+                          void* workspace, int64_t workspace_bytes, void* hip_stream) {
+  if (const char* why = mx::bad_matrix(t, n, dy_stride, dy_type)) return api_fail(CASGD_EINVAL, why);
+  if (const char* why = mx::bad_matrix(n, k, dw_stride, dw_type)) return api_fail(CASGD_EINVAL, why);
+  if (const char* why = mx::bad_codes(x_codes, x_scales, t, mx::kMx8)) return api_fail(CASGD_EINVAL, why);
+  if (const char* why = mx::bad_grad(t, n, k)) return api_fail(CASGD_EINVAL, why);
+  if (!dw || (t > 0 && (!dy || !workspace))) return api_fail(CASGD_EINVAL, "NULL pointer");
+  const mx::Plan p = mx::plan_of(true, t, n, k, dy_type, dy, dy_stride);
+  if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return api_fail(CASGD_EINVAL, "workspace must be 256-byte aligned");
+  if (workspace_bytes < p.c_bytes + p.x_bytes + p.s_bytes) return api_fail(CASGD_EINVAL, "workspace too small");
+  hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+  if (t == 0) {
+    if (accumulate) return CASGD_OK;
+    const unsigned grid = mx::grid_of(n * k);
+    if (dw_type == mx::kF32)
+      hipLaunchKernelGGL(mx::zero_kernel<float>, dim3(grid), dim3(mx::kThreads), 0, stream, static_cast<float*>(dw), n, k, dw_stride);
+    else
+      hipLaunchKernelGGL(mx::zero_kernel<uint16_t>, dim3(grid), dim3(mx::kThreads), 0, stream, static_cast<uint16_t*>(dw), n, k,
+                         dw_stride);
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? CASGD_OK : api_hip_fail(e, "weight gradient launch");
+  }
+  const hipError_t e = mx::run_grad<true, mx::kMx8>(p, dy, dy_type, dy_stride, x_codes, x_scales, dw, dw_type, dw_stride,
+                                                    accumulate, static_cast<uint8_t*>(workspace), stream);
+  return e == hipSuccess ? CASGD_OK : api_hip_fail(e, "weight gradient launch");
+}
+
+}  // extern "C"

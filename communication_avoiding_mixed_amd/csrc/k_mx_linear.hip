@@ -1,10 +1,4 @@
-// Products of a low-precision linear layer, simplest form: 64 x 64 output
-// tiles on the vector ALUs, each element of an operand read as float32 by an
-// accessor, 16 steps of the summed index at a time through LDS.
-//
-//   linear       y[m][n]  = sum_k Q4(x)[m][k] W4[n][k]
-//   grad input   dx[m][k] = sum_n dy[m][n] W4[n][k]
-//   grad weight  dW[n][k] = sum_t dy[t][n] Q8(x)[t][k]
+// y = Q4(x) W4^T with its C entry point: which of the product's forms runs.
 #include "casgd.h"
 #include "casgd_internal.h"
 #include "casgd_mx.h"
@@ -13,88 +7,6 @@
 namespace casgd {
 namespace mx {
 namespace {
-
-constexpr int kTile = 64, kStep = 16, kThreads = 256;
-
-template <int FMT>
-__device__ __forceinline__ float code_value(const uint8_t* codes, const uint8_t* scales, int64_t ld, int64_t row, int64_t col) {
-  const float s = scale_value(scales[row * (ld / kBlock) + col / kBlock]);
-  if constexpr (FMT == kMx4) {
-    const uint32_t c = (codes[row * (ld / 2) + (col >> 1)] >> (4 * (col & 1))) & 15u;
-    return __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0)[0] * s;
-  } else {
-    return e4m3_to_f32(codes[row * ld + col]) * s;
-  }
-}
-
-// operand(i, k): element of output row (or column) i at summed index k
-template <int FMT, bool ACROSS>
-struct Coded {
-  const uint8_t* codes;
-  const uint8_t* scales;
-  int64_t ld;
-  __device__ float operator()(int64_t i, int64_t k) const {
-    return ACROSS ? code_value<FMT>(codes, scales, ld, k, i) : code_value<FMT>(codes, scales, ld, i, k);
-  }
-};
-template <int TY, bool ACROSS>
-struct Plain {
-  const typename Elem<TY>::type* p;
-  int64_t stride;
-  __device__ float operator()(int64_t i, int64_t k) const { return load1<TY>(ACROSS ? p + k * stride + i : p + i * stride + k); }
-};
-
-template <int OUT, typename A, typename B>
-__global__ __launch_bounds__(kThreads) void product_kernel(A a, B b, int64_t rows, int64_t cols, int64_t depth,
-                                                          typename Elem<OUT>::type* __restrict__ out, int64_t stride,
-                                                          int accumulate) {
-  __shared__ float As[kStep][kTile + 1], Bs[kStep][kTile + 1];
-  const int64_t i0 = static_cast<int64_t>(blockIdx.y) * kTile, j0 = static_cast<int64_t>(blockIdx.x) * kTile;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < depth; k0 += kStep) {
-    for (int e = threadIdx.x; e < kTile * kStep; e += kThreads) {
-      const int i = e / kStep, k = e % kStep;
-      As[k][i] = i0 + i < rows && k0 + k < depth ? a(i0 + i, k0 + k) : 0.f;
-      Bs[k][i] = j0 + i < cols && k0 + k < depth ? b(j0 + i, k0 + k) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kStep; ++k)
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[u][q] = fmaf(As[k][ty * 4 + u], Bs[k][tx * 4 + q], acc[u][q]);
-    __syncthreads();
-  }
-#pragma unroll
-  for (int u = 0; u < 4; ++u)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int64_t i = i0 + ty * 4 + u, j = j0 + tx * 4 + q;
-      if (i < rows && j < cols) {
-        auto* p = out + i * stride + j;
-        store1<OUT>(p, accumulate ? load1<OUT>(p) + acc[u][q] : acc[u][q]);
-      }
-    }
-}
-
-template <int OUT, typename A, typename B>
-hipError_t run_as(A a, B b, int64_t rows, int64_t cols, int64_t depth, void* out, int64_t stride, int accumulate,
-                  hipStream_t stream) {
-  if (rows == 0 || cols == 0) return hipSuccess;
-  hipLaunchKernelGGL((product_kernel<OUT, A, B>), dim3((cols + kTile - 1) / kTile, (rows + kTile - 1) / kTile), dim3(kThreads),
-                     0, stream, a, b, rows, cols, depth, static_cast<typename Elem<OUT>::type*>(out), stride, accumulate);
-  return hipGetLastError();
-}
-
-template <typename A, typename B>
-hipError_t run_product(int type, A a, B b, int64_t rows, int64_t cols, int64_t depth, void* out, int64_t stride,
-                       int accumulate, hipStream_t stream) {
-  if (type == kBF16) return run_as<kBF16>(a, b, rows, cols, depth, out, stride, accumulate, stream);
-  if (type == kF16) return run_as<kF16>(a, b, rows, cols, depth, out, stride, accumulate, stream);
-  return run_as<kF32>(a, b, rows, cols, depth, out, stride, accumulate, stream);
-}
 
 constexpr int kSkinnyRows = 128;
 constexpr int64_t kMaxDepth = int64_t{1} << 24;  // 256 rows of codes stay below 2^32 bytes
@@ -201,50 +113,6 @@ int casgd_mx4_linear(const void* x, int x_type, int64_t m, int64_t k, int64_t x_
     if (e == hipSuccess) e = mx::launch_product(y_type, {codes, scales, m}, w, ld, y, y_stride, stream);
   }
   return e == hipSuccess ? CASGD_OK : api_hip_fail(e, "linear launch");
-}
-
-int casgd_mx4_grad_input(const void* dy, int dy_type, int64_t m, int64_t n, int64_t dy_stride, const uint8_t* w_codes,
-                         const uint8_t* w_scales, int64_t k, void* dx, int dx_type, int64_t dx_stride, void* hip_stream) {
-  if (const char* why = mx::bad_matrix(m, n, dy_stride, dy_type)) return api_fail(CASGD_EINVAL, why);
-  if (const char* why = mx::bad_matrix(m, k, dx_stride, dx_type)) return api_fail(CASGD_EINVAL, why);
-  if (const char* why = mx::bad_codes(w_codes, w_scales, n, mx::kMx4)) return api_fail(CASGD_EINVAL, why);
-  if (m == 0) return CASGD_OK;
-  if (!dy || !dx) return api_fail(CASGD_EINVAL, "NULL pointer");
-  const mx::Coded<mx::kMx4, true> w{w_codes, w_scales, mx::ld_of(k)};
-  hipStream_t stream = static_cast<hipStream_t>(hip_stream);
-  hipError_t e;
-  if (dy_type == mx::kBF16)
-    e = mx::run_product(dx_type, mx::Plain<mx::kBF16, false>{static_cast<const uint16_t*>(dy), dy_stride}, w, m, k, n, dx,
-                        dx_stride, 0, stream);
-  else if (dy_type == mx::kF16)
-    e = mx::run_product(dx_type, mx::Plain<mx::kF16, false>{static_cast<const uint16_t*>(dy), dy_stride}, w, m, k, n, dx,
-                        dx_stride, 0, stream);
-  else
-    e = mx::run_product(dx_type, mx::Plain<mx::kF32, false>{static_cast<const float*>(dy), dy_stride}, w, m, k, n, dx,
-                        dx_stride, 0, stream);
-  return e == hipSuccess ? CASGD_OK : api_hip_fail(e, "input gradient launch");
-}
-
-int casgd_mx8_grad_weight(const void* dy, int dy_type, int64_t t, int64_t n, int64_t dy_stride, const uint8_t* x_codes,
-                          const uint8_t* x_scales, int64_t k, void* dw, int dw_type, int64_t dw_stride, int accumulate,
-                          void* hip_stream) {
-  if (const char* why = mx::bad_matrix(t, n, dy_stride, dy_type)) return api_fail(CASGD_EINVAL, why);
-  if (const char* why = mx::bad_matrix(n, k, dw_stride, dw_type)) return api_fail(CASGD_EINVAL, why);
-  if (const char* why = mx::bad_codes(x_codes, x_scales, t, mx::kMx8)) return api_fail(CASGD_EINVAL, why);
-  if (!dw || (t > 0 && !dy)) return api_fail(CASGD_EINVAL, "NULL pointer");
-  const mx::Coded<mx::kMx8, true> x{x_codes, x_scales, mx::ld_of(k)};
-  hipStream_t stream = static_cast<hipStream_t>(hip_stream);
-  hipError_t e;
-  if (dy_type == mx::kBF16)
-    e = mx::run_product(dw_type, mx::Plain<mx::kBF16, true>{static_cast<const uint16_t*>(dy), dy_stride}, x, n, k, t, dw,
-                        dw_stride, accumulate, stream);
-  else if (dy_type == mx::kF16)
-    e = mx::run_product(dw_type, mx::Plain<mx::kF16, true>{static_cast<const uint16_t*>(dy), dy_stride}, x, n, k, t, dw,
-                        dw_stride, accumulate, stream);
-  else
-    e = mx::run_product(dw_type, mx::Plain<mx::kF32, true>{static_cast<const float*>(dy), dy_stride}, x, n, k, t, dw,
-                        dw_stride, accumulate, stream);
-  return e == hipSuccess ? CASGD_OK : api_hip_fail(e, "weight gradient launch");
 }
 
 }  // extern "C"

@@ -365,12 +365,19 @@ int casgd_mx4_linear(const void* x, int x_type, int64_t m, int64_t k, int64_t x_
  *   casgd_mx8_grad_weight  dW (n x k) = dy^T X, X (t x k) the activations
  *                          checkpointed in MX8 (the rounding of Q4 taken as
  *                          the identity); accumulate != 0 adds to dw.  t = 0
- *                          gives zeros (or leaves dw). */
+ *                          gives zeros (or leaves dw).
+ * n, k <= 2^22.  workspace: casgd_mx_grad_workspace bytes at least, 256-byte
+ * aligned, of the same arguments (weight: 0 for the input's gradient, 1 for
+ * the weights', whose t is m; dy is only looked at for its alignment): the
+ * coded matrix as bf16, and a copy of dy unless it is bf16 with 16-byte
+ * aligned rows. */
+int64_t casgd_mx_grad_workspace(int weight, int64_t m, int64_t n, int64_t k, const void* dy, int dy_type, int64_t dy_stride);
 int casgd_mx4_grad_input(const void* dy, int dy_type, int64_t m, int64_t n, int64_t dy_stride, const uint8_t* w_codes,
-                         const uint8_t* w_scales, int64_t k, void* dx, int dx_type, int64_t dx_stride, void* hip_stream);
+                         const uint8_t* w_scales, int64_t k, void* dx, int dx_type, int64_t dx_stride, void* workspace,
+                         int64_t workspace_bytes, void* hip_stream);
 int casgd_mx8_grad_weight(const void* dy, int dy_type, int64_t t, int64_t n, int64_t dy_stride, const uint8_t* x_codes,
                           const uint8_t* x_scales, int64_t k, void* dw, int dw_type, int64_t dw_stride, int accumulate,
-                          void* hip_stream);
+                          void* workspace, int64_t workspace_bytes, void* hip_stream);
 
 /* Log probabilities of the labelled tokens: logps[t] = z_t[y_t] -
  * log sum_v exp z_t[v], float32, from logits z (tokens x vocab).

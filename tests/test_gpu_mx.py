@@ -175,6 +175,18 @@ def test_gradients(m, n, k):
         assert torch.equal(got, B.mx8_grad_weight(strided(dy, 5, 3), x, out_dtype=T[out]))
 
 
+@pytest.mark.parametrize("m,n,k", [(70, 3900, 4200), (3900, 65, 4200), (3900, 4200, 90), (1000, 1003, 1500), (4096, 40, 3900)])
+def test_gradients_of_many_tiles(m, n, k):
+    w, x = stored(values((n, k), 4), "mx4"), stored(values((m, k), 5), "mx8")
+    wv = H.dequantize(w.codes.cpu().numpy(), w.scales.cpu().numpy(), k, "mx4")
+    xv = H.dequantize(x.codes.cpu().numpy(), x.scales.cpu().numpy(), k, "mx8")
+    for dtype, out in (("bf16", "bf16"), ("fp32", "fp32")):
+        dy = cuda(values((m, n), 6) * 0.01, dtype)
+        dyv = host(dy)
+        close(B.mx4_grad_input(dy, w, T[out]), dyv, wv, out)
+        close(B.mx8_grad_weight(dy, x, out_dtype=T[out]), dyv.T, xv, out)
+
+
 def test_gradient_of_no_rows():
     x = B.mx_quantize(torch.empty((0, 40), device="cuda"), "mx8")
     dy = torch.empty((0, 6), device="cuda")

@@ -53,12 +53,33 @@ def test_product_refusals():
     linear(0, None, "NULL"), linear(8, None, "NULL"), linear(11, None, "NULL"), linear(5, None, "NULL")
     linear(1, 3, "element type"), linear(9, 7, "element type"), linear(4, 63, "row stride"), linear(10, 7, "row stride")
     linear(12, need - 1, "workspace"), linear(11, ODD, "aligned"), linear(5, ODD, "aligned"), linear(7, 0, "columns")
-    refused(lib.casgd_mx4_grad_input(P, B.FP32, 4, 8, 7, P, P, 64, P, B.FP32, 64, None), "row stride")
-    refused(lib.casgd_mx4_grad_input(None, B.FP32, 4, 8, 8, P, P, 64, P, B.FP32, 64, None), "NULL")
-    refused(lib.casgd_mx4_grad_input(P, B.FP32, 4, 8, 8, P, P, 64, P, B.FP8, 64, None), "element type")
-    refused(lib.casgd_mx8_grad_weight(P, B.FP32, 4, 8, 8, P, P, 64, None, B.FP32, 64, 0, None), "NULL")
-    refused(lib.casgd_mx8_grad_weight(P, B.FP32, 4, 8, 8, P, P, 64, P, B.FP32, 63, 0, None), "row stride")
-    refused(lib.casgd_mx8_grad_weight(P, B.FP32, 4, 8, 8, None, P, 64, P, B.FP32, 64, 0, None), "NULL")
+
+
+def test_gradient_refusals():
+    lib = B.load()
+    need = lib.casgd_mx_grad_workspace(0, 4, 8, 64, P, B.FP32, 8)
+    assert need >= 32 * 128 * 2 and lib.casgd_mx_grad_workspace(0, 4, 8, 64, P, B.FP8, 8) == -1
+    ok = (P, B.FP32, 4, 8, 8, P, P, 64, P, B.FP32, 64, P, need, None)
+
+    def grad_input(at, value, text):
+        refused(lib.casgd_mx4_grad_input(*ok[:at], value, *ok[at + 1:]), text)
+
+    for at in (0, 5, 6, 8, 11):
+        grad_input(at, None, "NULL")
+    grad_input(1, B.FP8, "element type"), grad_input(9, 9, "element type"), grad_input(4, 7, "row stride")
+    grad_input(10, 63, "row stride"), grad_input(12, need - 1, "workspace"), grad_input(11, ODD, "aligned")
+    grad_input(2, 2 ** 30, "rows")
+    need = lib.casgd_mx_grad_workspace(1, 4, 8, 64, P, B.FP32, 8)
+    okw = (P, B.FP32, 4, 8, 8, P, P, 64, P, B.FP32, 64, 0, P, need, None)
+
+    def grad_weight(at, value, text):
+        refused(lib.casgd_mx8_grad_weight(*okw[:at], value, *okw[at + 1:]), text)
+
+    for at in (0, 5, 6, 8, 12):
+        grad_weight(at, None, "NULL")
+    grad_weight(1, B.FP8, "element type"), grad_weight(9, 9, "element type"), grad_weight(4, 7, "row stride")
+    grad_weight(10, 63, "row stride"), grad_weight(13, need - 1, "workspace"), grad_weight(12, ODD, "aligned")
+    refused(lib.casgd_mx4_grad_input(P, B.BF16, 4, 2 ** 23, 2 ** 23, P, P, 64, P, B.BF16, 64, P, need, None), "2^22")
 
 
 def test_preference_refusals():
