@@ -12,6 +12,7 @@ import ctypes
 import os
 
 import numpy as np
+import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libcasgd.so")
@@ -298,14 +299,17 @@ def unpack_gram(G_packed: np.ndarray, s: int, b: int) -> dict:
 
 
 # -- operators of a low-precision linear layer and its preference loss
+#
+# A small call's time is mostly its host side, so these keep it short: results
+# of one call share one allocation, views of it are made when asked for, and
+# the stream is taken as the raw handle.
 
-_TYPES = {}  # torch dtype -> element type id
+_TYPES = {torch.bfloat16: BF16, torch.float32: FP32, torch.float16: FP16}
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+_current_device = torch.cuda.current_device
 
 
 def _type_id(dtype, name):
-    if not _TYPES:
-        import torch
-        _TYPES.update({torch.bfloat16: BF16, torch.float32: FP32, torch.float16: FP16})
     t = _TYPES.get(dtype)
     if t is None:
         raise ValueError(f"{name} must be bfloat16, float16 or float32, not {dtype}")
@@ -324,7 +328,7 @@ def _rows_of(t, name):
         raise ValueError(f"{name} must have at least one column")
     if (step != 1 and cols > 1) or (stride < cols and rows > 1):
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
-    return _type_id(t.dtype, name), rows, cols, max(stride, cols)
+    return _type_id(t.dtype, name), rows, cols, stride if stride > cols else cols
 
 
 def _vector(t, dtype, count, name, device):
@@ -333,15 +337,15 @@ def _vector(t, dtype, count, name, device):
     return t.data_ptr()
 
 
-def _call(device, entry, *args):
+def _queue(entry: str, device, *args):
     """Call an entry point on torch's current stream of the tensors' device."""
-    import torch
     fn = getattr(_lib or load(), entry)
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+    index = device.index
+    if index == _current_device():
+        rc = fn(*args, _raw_stream(index))
     else:
-        rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.device(index):
+            rc = fn(*args, _raw_stream(index))
     if rc != OK:
         _check(rc, entry)
 
@@ -355,20 +359,20 @@ class MXMatrix:
     """A rows x cols matrix in a microscaled format (see include/casgd.h).
 
     fmt: "mx4" or "mx8"; codes uint8 [rows, ld / 2] or [rows, ld], scales
-    uint8 [rows, ld / 32], ld = mx_ld(cols); both contiguous on one GPU.
+    uint8 [rows, ld / 32], ld = mx_ld(cols); both contiguous on one GPU, codes
+    16-byte and scales 4-byte aligned.
     """
 
-    __slots__ = ("fmt", "codes", "scales", "rows", "cols")
+    __slots__ = ("fmt", "rows", "cols", "device", "_codes", "_scales", "_hold")
 
     def __init__(self, fmt: str, codes, scales, cols: int):
-        import torch
         if fmt not in MX_FORMATS:
             raise ValueError(f"fmt must be one of {sorted(MX_FORMATS)}")
         if cols < 1:
             raise ValueError("cols must be at least 1")
         ld = mx_ld(cols)
         rows = codes.shape[0]
-        if tuple(codes.shape) != (rows, ld // 2 if fmt == "mx4" else ld) or tuple(scales.shape) != (rows, ld // 32):
+        if codes.shape != (rows, ld // 2 if fmt == "mx4" else ld) or scales.shape != (rows, ld // 32):
             raise ValueError(f"codes and scales do not fit rows of {cols} elements in {fmt}")
         if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
             raise ValueError("codes and scales must be uint8")
@@ -376,75 +380,94 @@ class MXMatrix:
             raise ValueError("codes and scales must be on one GPU")
         if not (codes.is_contiguous() and scales.is_contiguous()):
             raise ValueError("codes and scales must be contiguous")
-        self.fmt, self.codes, self.scales, self.rows, self.cols = fmt, codes, scales, rows, int(cols)
+        self.fmt, self.rows, self.cols, self.device = fmt, rows, int(cols), codes.device
+        self._codes, self._scales, self._hold = codes.data_ptr(), scales.data_ptr(), (codes, scales)
+
+    def _parts(self):
+        if not isinstance(self._hold, tuple):  # one allocation: codes, then scales
+            ld = mx_ld(self.cols)
+            split = self.rows * (ld // 2 if self.fmt == "mx4" else ld)
+            self._hold = (self._hold[:split].view(self.rows, split // self.rows if self.rows else ld),
+                          self._hold[split:].view(self.rows, ld // 32))
+        return self._hold
+
+    @property
+    def codes(self):
+        return self._parts()[0]
+
+    @property
+    def scales(self):
+        return self._parts()[1]
 
     def _need(self, fmt, name, device):
         if self.fmt != fmt:
             raise ValueError(f"{name} must be in {fmt}")
-        if self.codes.device != device:
+        if self.device != device:
             raise ValueError(f"{name} must be on {device}")
 
 
 def mx_quantize(x, fmt: str) -> MXMatrix:
     """x (a GPU matrix of bf16, fp16 or float32) in a microscaled format."""
-    import torch
     ty, rows, cols, stride = _rows_of(x, "x")
     if fmt not in MX_FORMATS:
         raise ValueError(f"fmt must be one of {sorted(MX_FORMATS)}")
-    ld = mx_ld(cols)
-    codes = torch.empty((rows, ld // 2 if fmt == "mx4" else ld), dtype=torch.uint8, device=x.device)
-    scales = torch.empty((rows, ld // 32), dtype=torch.uint8, device=x.device)
-    _call(x.device, "casgd_mx_quantize", x.data_ptr(), ty, rows, cols, stride, MX_FORMATS[fmt], codes.data_ptr(),
-          scales.data_ptr())
-    return MXMatrix(fmt, codes, scales, cols)
+    q = MXMatrix.__new__(MXMatrix)
+    q.fmt, q.rows, q.cols, q.device = fmt, rows, cols, x.device
+    ld = (cols + 127) // 128 * 128
+    split = rows * (ld // 2 if fmt == "mx4" else ld)
+    q._hold = torch.empty(split + rows * (ld // 32), dtype=torch.uint8, device=q.device)
+    q._codes = q._hold.data_ptr()
+    q._scales = q._codes + split
+    _queue("casgd_mx_quantize", q.device, x.data_ptr(), ty, rows, cols, stride, MX_FORMATS[fmt], q._codes, q._scales)
+    return q
 
 
 def mx_dequantize(q: MXMatrix, dtype):
     """The values of a microscaled matrix, rounded to dtype."""
-    import torch
     ty = _type_id(dtype, "dtype")
-    device = q.codes.device
-    out = torch.empty((q.rows, q.cols), dtype=dtype, device=device)
-    _call(device, "casgd_mx_dequantize", q.codes.data_ptr(), q.scales.data_ptr(), MX_FORMATS[q.fmt], q.rows, q.cols,
-          out.data_ptr(), ty, q.cols)
+    out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.device)
+    _queue("casgd_mx_dequantize", q.device, q._codes, q._scales, MX_FORMATS[q.fmt], q.rows, q.cols, out.data_ptr(), ty,
+           q.cols)
     return out
 
 
 def mx4_linear(x, w: MXMatrix, out_dtype=None):
     """y = Q4(x) W^T for x [m, k] and W [n, k] kept in mx4; y of out_dtype (x's by default)."""
-    import torch
     ty, m, k, stride = _rows_of(x, "x")
     device = x.device
     w._need("mx4", "w", device)
     if w.cols != k:
         raise ValueError(f"x has {k} columns and w {w.cols}")
-    out_dtype = out_dtype or x.dtype
-    out_ty = _type_id(out_dtype, "out_dtype")
-    y = torch.empty((m, w.rows), dtype=out_dtype, device=device)
-    if y.numel() == 0:
+    if out_dtype is None:
+        out_dtype = x.dtype
+    out_ty, n = _type_id(out_dtype, "out_dtype"), w.rows
+    y = torch.empty((m, n), dtype=out_dtype, device=device)
+    if m == 0 or n == 0:
         return y
-    need = load().casgd_mx4_linear_workspace(m, k, w.rows)
-    ws = torch.empty(need, dtype=torch.uint8, device=device)
-    _call(device, "casgd_mx4_linear", x.data_ptr(), ty, m, k, stride, w.codes.data_ptr(), w.scales.data_ptr(), w.rows,
-          y.data_ptr(), out_ty, w.rows, ws.data_ptr(), need)
+    need = (_lib or load()).casgd_mx4_linear_workspace(m, k, n)
+    ws = torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
+    _queue("casgd_mx4_linear", device, x.data_ptr(), ty, m, k, stride, w._codes, w._scales, n, y.data_ptr(), out_ty, n,
+           ws.data_ptr() if need > 0 else None, need)
     return y
 
 
 def mx4_grad_input(dy, w: MXMatrix, out_dtype=None):
     """dx = dy W for dy [m, n] and W [n, k] kept in mx4; dx of out_dtype (dy's by default)."""
-    import torch
     ty, m, n, stride = _rows_of(dy, "dy")
     device = dy.device
     w._need("mx4", "w", device)
     if w.rows != n:
         raise ValueError(f"dy has {n} columns and w {w.rows} rows")
-    out_dtype = out_dtype or dy.dtype
-    out_ty = _type_id(out_dtype, "out_dtype")
-    dx = torch.empty((m, w.cols), dtype=out_dtype, device=device)
-    need = load().casgd_mx_grad_workspace(0, m, n, w.cols, dy.data_ptr(), ty, stride)
-    ws = torch.empty(max(need, 0), dtype=torch.uint8, device=device)
-    _call(device, "casgd_mx4_grad_input", dy.data_ptr(), ty, m, n, stride, w.codes.data_ptr(), w.scales.data_ptr(),
-          w.cols, dx.data_ptr(), out_ty, w.cols, ws.data_ptr(), need)
+    if out_dtype is None:
+        out_dtype = dy.dtype
+    out_ty, k = _type_id(out_dtype, "out_dtype"), w.cols
+    dx = torch.empty((m, k), dtype=out_dtype, device=device)
+    if m == 0:
+        return dx
+    need = (_lib or load()).casgd_mx_grad_workspace(0, m, n, k, dy.data_ptr(), ty, stride)
+    ws = torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
+    _queue("casgd_mx4_grad_input", device, dy.data_ptr(), ty, m, n, stride, w._codes, w._scales, k, dx.data_ptr(), out_ty,
+           k, ws.data_ptr() if need > 0 else None, need)
     return dx
 
 
@@ -454,43 +477,66 @@ def mx8_grad_weight(dy, x: MXMatrix, out=None, accumulate: bool = False, out_dty
     out: the [n, k] result (float32 unless out_dtype says otherwise);
     accumulate adds to it.
     """
-    import torch
     ty, t, n, stride = _rows_of(dy, "dy")
     device = dy.device
     x._need("mx8", "x", device)
     if x.rows != t:
         raise ValueError(f"dy has {t} rows and x {x.rows}")
+    k = x.cols
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = torch.empty((n, x.cols), dtype=out_dtype or torch.float32, device=device)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError("out and out_dtype disagree")
-    out_ty, rows, cols, out_stride = _rows_of(out, "out")
-    if (rows, cols) != (n, x.cols) or out.device != device:
-        raise ValueError(f"out must be {n} x {x.cols} on {device}")
-    need = load().casgd_mx_grad_workspace(1, t, n, x.cols, dy.data_ptr(), ty, stride)
-    ws = torch.empty(max(need, 0), dtype=torch.uint8, device=device)
-    _call(device, "casgd_mx8_grad_weight", dy.data_ptr(), ty, t, n, stride, x.codes.data_ptr(), x.scales.data_ptr(),
-          x.cols, out.data_ptr(), out_ty, out_stride, 1 if accumulate else 0, ws.data_ptr(), need)
+        out = torch.empty((n, k), dtype=out_dtype or torch.float32, device=device)
+        out_ty, out_stride = _type_id(out.dtype, "out_dtype"), k
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out and out_dtype disagree")
+        out_ty, rows, cols, out_stride = _rows_of(out, "out")
+        if (rows, cols) != (n, k) or out.device != device:
+            raise ValueError(f"out must be {n} x {k} on {device}")
+    need = (_lib or load()).casgd_mx_grad_workspace(1, t, n, k, dy.data_ptr(), ty, stride)
+    ws = torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
+    _queue("casgd_mx8_grad_weight", device, dy.data_ptr(), ty, t, n, stride, x._codes, x._scales, k, out.data_ptr(),
+           out_ty, out_stride, 1 if accumulate else 0, ws.data_ptr() if need > 0 else None, need)
     return out
 
 
 def token_logps(logits, labels):
     """Log probability of each row's label (int64; negative: masked, 0)."""
-    import torch
     ty, t, v, stride = _rows_of(logits, "logits")
     device = logits.device
     pl = _vector(labels, torch.int64, t, "labels", device)
     logps = torch.empty(t, dtype=torch.float32, device=device)
-    _call(device, "casgd_token_logps", logits.data_ptr(), ty, t, v, stride, pl, logps.data_ptr())
+    _queue("casgd_token_logps", device, logits.data_ptr(), ty, t, v, stride, pl, logps.data_ptr())
     return logps
 
 
 class PrefLoss:
-    """What pref_loss returns: loss and margin per pair, logps per token, and what pref_grad needs."""
+    """What pref_loss returns: loss and margin [pairs], logps [tokens], stats
+    [tokens, 2] and slope [2 pairs] (float32), and the inputs that pref_grad reads again."""
 
-    __slots__ = ("loss", "margin", "logps", "stats", "slope", "logits", "labels", "offsets", "pairs")
+    __slots__ = ("logits", "labels", "offsets", "pairs", "tokens", "_buf")
+
+    # one float32 allocation: workspace (2 tokens), stats (2 tokens), logps (tokens), loss, margin, slope (2 pairs)
+    @property
+    def stats(self):
+        return self._buf.narrow(0, 2 * self.tokens, 2 * self.tokens).view(self.tokens, 2)
+
+    @property
+    def logps(self):
+        return self._buf.narrow(0, 4 * self.tokens, self.tokens)
+
+    @property
+    def loss(self):
+        return self._buf.narrow(0, 5 * self.tokens, self.pairs)
+
+    @property
+    def margin(self):
+        return self._buf.narrow(0, 5 * self.tokens + self.pairs, self.pairs)
+
+    @property
+    def slope(self):
+        return self._buf.narrow(0, 5 * self.tokens + 2 * self.pairs, 2 * self.pairs)
 
 
 def pref_loss(logits, labels, offsets, ref_logps=None, beta: float = 0.1, loss: str = "logistic",
@@ -502,7 +548,6 @@ def pref_loss(logits, labels, offsets, ref_logps=None, beta: float = 0.1, loss: 
     turn; ref_logps float32 [tokens] or None; loss "logistic" or "squared".
     The result keeps references to logits, labels and offsets for pref_grad.
     """
-    import torch
     if loss not in ("logistic", "squared"):
         raise ValueError("loss must be logistic or squared")
     ty, t, v, stride = _rows_of(logits, "logits")
@@ -514,31 +559,30 @@ def pref_loss(logits, labels, offsets, ref_logps=None, beta: float = 0.1, loss: 
     po = _vector(offsets, torch.int64, count, "offsets", device)
     pr = None if ref_logps is None else _vector(ref_logps, torch.float32, t, "ref_logps", device)
     r = PrefLoss()
-    r.pairs, r.logits, r.labels, r.offsets = count // 2, logits, labels, offsets
-    r.loss = torch.empty(r.pairs, dtype=torch.float32, device=device)
-    r.margin = torch.empty(r.pairs, dtype=torch.float32, device=device)
-    r.slope = torch.empty(2 * r.pairs, dtype=torch.float32, device=device)
-    r.logps = torch.empty(t, dtype=torch.float32, device=device)
-    r.stats = torch.empty((t, 2), dtype=torch.float32, device=device)
-    ws = torch.empty(t, dtype=torch.float64, device=device)
-    _call(device, "casgd_pref_loss", logits.data_ptr(), ty, t, v, stride, pl, po, r.pairs, pr, LOSS_IDS[loss], beta,
-          smoothing, 1 if average else 0, r.loss.data_ptr(), r.margin.data_ptr(), r.logps.data_ptr(),
-          r.stats.data_ptr(), r.slope.data_ptr(), ws.data_ptr(), 8 * t)
+    pairs = count // 2
+    r.pairs, r.tokens, r.logits, r.labels, r.offsets = pairs, t, logits, labels, offsets
+    r._buf = torch.empty(5 * t + 4 * pairs, dtype=torch.float32, device=device)
+    ws = r._buf.data_ptr()
+    _queue("casgd_pref_loss", device, logits.data_ptr(), ty, t, v, stride, pl, po, pairs, pr, LOSS_IDS[loss], beta,
+           smoothing, 1 if average else 0, ws + 20 * t, ws + 20 * t + 4 * pairs, ws + 16 * t, ws + 8 * t,
+           ws + 20 * t + 8 * pairs, ws, 8 * t)
     return r
 
 
 def pref_grad(fwd: PrefLoss, grad_loss, out=None):
     """Gradient of sum(grad_loss * loss) in the logits; out may be fwd.logits itself."""
-    import torch
     logits = fwd.logits
     ty, t, v, stride = _rows_of(logits, "logits")
     device = logits.device
     pg = _vector(grad_loss, torch.float32, fwd.pairs, "grad_loss", device)
     if out is None:
         out = torch.empty((t, v), dtype=logits.dtype, device=device)
-    out_ty, rows, cols, out_stride = _rows_of(out, "out")
-    if (out_ty, rows, cols) != (ty, t, v) or out.device != device:
-        raise ValueError(f"out must be {t} x {v} of {logits.dtype} on {device}")
-    _call(device, "casgd_pref_grad", logits.data_ptr(), ty, t, v, stride, fwd.labels.data_ptr(),
-          fwd.offsets.data_ptr(), fwd.pairs, fwd.stats.data_ptr(), fwd.slope.data_ptr(), pg, out.data_ptr(), out_stride)
+        out_stride = v
+    else:
+        out_ty, rows, cols, out_stride = _rows_of(out, "out")
+        if (out_ty, rows, cols) != (ty, t, v) or out.device != device:
+            raise ValueError(f"out must be {t} x {v} of {logits.dtype} on {device}")
+    ws = fwd._buf.data_ptr()
+    _queue("casgd_pref_grad", device, logits.data_ptr(), ty, t, v, stride, fwd.labels.data_ptr(),
+           fwd.offsets.data_ptr(), fwd.pairs, ws + 8 * t, ws + 20 * t + 8 * fwd.pairs, pg, out.data_ptr(), out_stride)
     return out

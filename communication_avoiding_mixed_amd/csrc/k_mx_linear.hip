@@ -80,6 +80,7 @@ extern "C" {
 
 int64_t casgd_mx4_linear_workspace(int64_t m, int64_t k, int64_t n) {
   if (m < 0 || m > mx::kMaxDim || k < 1 || k > mx::kMaxDim || n < 0 || n > mx::kMaxDim) return -1;
+  if (mx::decodes(m, k, n)) return 0;
   const int64_t ld = mx::ld_of(k);
   return m * (ld / 2 + ld / mx::kBlock);
 }
@@ -92,9 +93,10 @@ int casgd_mx4_linear(const void* x, int x_type, int64_t m, int64_t k, int64_t x_
   if (const char* why = mx::bad_codes(w_codes, w_scales, n, mx::kMx4)) return api_fail(CASGD_EINVAL, why);
   if (k > mx::kMaxDepth) return api_fail(CASGD_EINVAL, "k exceeds 2^24");
   if (m == 0) return CASGD_OK;
-  if (!x || !y || !workspace) return api_fail(CASGD_EINVAL, "NULL pointer");
+  const int64_t need = casgd_mx4_linear_workspace(m, k, n);
+  if (!x || !y || (need > 0 && !workspace)) return api_fail(CASGD_EINVAL, "NULL pointer");
   if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0) return api_fail(CASGD_EINVAL, "workspace must be 16-byte aligned");
-  if (workspace_bytes < casgd_mx4_linear_workspace(m, k, n)) return api_fail(CASGD_EINVAL, "workspace too small");
+  if (workspace_bytes < need) return api_fail(CASGD_EINVAL, "workspace too small");
   hipStream_t stream = static_cast<hipStream_t>(hip_stream);
   const int64_t ld = mx::ld_of(k);
   uint8_t* codes = static_cast<uint8_t*>(workspace);

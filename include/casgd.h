@@ -352,7 +352,7 @@ int casgd_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int format,
 /* y = Q4(x) W^T: x (m x k) is quantised to MX4 as by casgd_mx_quantize, W
  * (n x k) is kept in MX4; float32 sums, rounded once to y's type (m x n).
  * k <= 2^24.  workspace: casgd_mx4_linear_workspace(m, k, n) bytes at
- * least, 16-byte aligned, free again when the call's work is done.
+ * least (0: none), 16-byte aligned, free again when the call's work is done.
  * Bit-identical on repeats. */
 int64_t casgd_mx4_linear_workspace(int64_t m, int64_t k, int64_t n);
 int casgd_mx4_linear(const void* x, int x_type, int64_t m, int64_t k, int64_t x_stride, const uint8_t* w_codes,

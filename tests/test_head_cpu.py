@@ -43,9 +43,10 @@ def test_quantise_refusals(args, text):
 
 def test_product_refusals():
     lib = B.load()
-    need = lib.casgd_mx4_linear_workspace(4, 64, 8)
-    assert need > 0 and lib.casgd_mx4_linear_workspace(4, 0, 8) == -1
-    ok = (P, B.BF16, 4, 64, 64, P, P, 8, P, B.BF16, 8, P, need, None)
+    assert lib.casgd_mx4_linear_workspace(4, 64, 8) == 0 and lib.casgd_mx4_linear_workspace(4, 0, 8) == -1
+    need = lib.casgd_mx4_linear_workspace(40, 64, 8)
+    assert need >= 40 * (64 + 4)
+    ok = (P, B.BF16, 40, 64, 64, P, P, 8, P, B.BF16, 8, P, need, None)
 
     def linear(at, value, text):
         refused(lib.casgd_mx4_linear(*ok[:at], value, *ok[at + 1:]), text)
