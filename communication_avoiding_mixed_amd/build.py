@@ -24,7 +24,7 @@ LIB = os.path.join(PKG, "libcasgd.so")
 SOURCES = ["casgd_api.hip", "k_gather.hip", "k_gram.hip", "k_chain.hip", "k_chain_la.hip", "k_loss.hip",
            "k_step.hip", "k_step_1x1.hip", "k_step_2x1.hip", "k_step_2x2.hip", "k_step_4x2.hip",
            "k_step_4x4.hip", "k_peak.hip", "k_mx.hip", "k_mx_linear.hip", "k_mx_grad.hip", "k_pref.hip"]
-HEADERS = ["casgd_device.h", "casgd_internal.h", "casgd_chain.h", "casgd_mx.h", "casgd_mx_gemm.h", "casgd_mx_grad.h"]
+HEADERS = ["casgd_device.h", "casgd_internal.h", "casgd_chain.h", "casgd_mx.h", "casgd_mx_gemm.h", "casgd_mx_grad.h", "casgd_mx_small.h"]
 
 ARCH = "gfx950"
 FLAGS = [

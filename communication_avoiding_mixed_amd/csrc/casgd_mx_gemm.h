@@ -18,13 +18,15 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// vmcnt(n) alone: the other counters at their maximum
+// Wait until at most N of the wave's loads are on their way, or until its LDS
+// accesses are done.  As asm with a memory clobber, so that no LDS access moves
+// across.
 template <int N>
 __device__ __forceinline__ void wait_vm() {
   static_assert(N >= 0 && N < 64, "vmcnt");
-  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (3 << 14)); }
+__device__ __forceinline__ void wait_lgkm0() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 // Direct-to-LDS load, 16 bytes a lane: lane i's bytes at base + off go to LDS
 // at lds + 16 i.  No register result; the data is there after this wave's
@@ -33,6 +35,10 @@ __device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(15 | (
 // would leave one stage in flight; the waits here are explicit.
 __device__ __forceinline__ void load_lds16(uint32_t lds, const void* base, uint32_t off) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+}
+
+__device__ __forceinline__ void load_lds4(uint32_t lds, const void* base, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
 }
 
 __device__ __forceinline__ f32x16 mfma_mx4_32(i32x4 a, i32x4 b, f32x16 c, int sa, int sb, int which) {
@@ -149,8 +155,8 @@ constexpr int gemm_lds_bytes() {
 //
 // Codes travel through a ring of four stages by direct-to-LDS loads, three
 // stages ahead; a row's 64 bytes are four 16-byte pieces, stored at piece
-// number XOR (row / 2 mod 4), so that 8 lanes reading one piece of 8 rows touch
-// all banks.  Fragments are read half a stage ahead of their instructions, and
+// number XOR (row / 4 mod 4), so that the 16 lanes that read one piece of 16
+// rows in a cycle touch all 64 banks.  Fragments are read half a stage ahead of their instructions, and
 // the barrier that frees a ring slot sits between the halves, behind queued
 // matrix work.
 //
@@ -187,7 +193,7 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void mx4_gemm_kernel(Mx4Operand x,
     const int first = is_w ? g * 16 : g * 16 - RW;
     const int64_t left = is_w ? w.rows - n0 : x.rows - m0;
     int r = first + (lane >> 2);
-    const int piece = (lane & 3) ^ ((r >> 1) & 3);
+    const int piece = (lane & 3) ^ ((r >> 2) & 3);
     if (r >= left) r = static_cast<int>(left) - 1;
     cbase[i] = is_w ? w.codes + n0 * cpitch : x.codes + m0 * cpitch;
     coff[i] = static_cast<uint32_t>(r * cpitch) + piece * 16;
@@ -234,7 +240,7 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void mx4_gemm_kernel(Mx4Operand x,
 
   const int wn = wave / GM, wm = wave % GM;
   const int half = lane >> 5, r32 = lane & 31;
-  const int sw = (r32 >> 1) & 3;
+  const int sw = (r32 >> 2) & 3;
   // byte offsets of this lane's fragment rows and scales inside a stage
   const int wrow = wn * 32 * WN + r32, xrow = RW + wm * 32 * WM + r32;
   const int piece[2] = {((2 * half) ^ sw) * 16, ((2 * half + 1) ^ sw) * 16};
@@ -325,55 +331,12 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void mx4_gemm_kernel(Mx4Operand x,
   store_tile<OUT, WM, WN>(acc, smem + wave * 32 * PITCH, y, stride, m0 + wm * 32 * WM, n0 + wn * 32 * WN, x.rows, w.rows, 0);
 }
 
-// Few rows of x: y[m][n], m < 32 MT, for 32 rows of W a workgroup.  Every byte
-// of W is used by one wave only, so its fragments come straight from memory;
-// the 8 waves share the summed index, 256 elements (one 128-byte line of a row)
-// a turn, and their sums meet in LDS in a fixed order.  Bound by reading W; x
-// is read by every workgroup, from the L2s.
-template <int OUT, int MT>
-__global__ __launch_bounds__(512) void mx4_skinny_kernel(Mx4Operand x, Mx4Operand w, int64_t ld,
-                                                        typename Elem<OUT>::type* __restrict__ y, int64_t stride) {
-  __shared__ float part[8][16][64];
+// The waves' sums of 32 MT rows of x by 32 rows of W (from row n0), added in
+// order and stored.  part: 4 KB a wave.
+template <int OUT, int MT, int WAVES>
+__device__ __forceinline__ void join_waves(const f32x16 (&acc)[MT], float (*part)[16][64], typename Elem<OUT>::type* y,
+                                           int64_t stride, int64_t n0, int64_t m_rows, int64_t n_rows) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int half = lane >> 5, r32 = lane & 31;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 32;
-  const int64_t cpitch = ld / 2, spitch = ld / 32;
-  const int64_t wr = n0 + r32 < w.rows ? n0 + r32 : w.rows - 1;
-  const uint8_t* wc = w.codes + wr * cpitch + half * 64;
-  const uint8_t* ws = w.scales + wr * spitch + half * 4;
-  const uint8_t* xc[MT];
-  const uint8_t* xs[MT];
-#pragma unroll
-  for (int b = 0; b < MT; ++b) {
-    const int64_t r = b * 32 + r32 < x.rows ? b * 32 + r32 : x.rows - 1;
-    xc[b] = x.codes + r * cpitch + half * 64;
-    xs[b] = x.scales + r * spitch + half * 4;
-  }
-  f32x16 acc[MT];
-#pragma unroll
-  for (int b = 0; b < MT; ++b)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) acc[b][e] = 0.f;
-
-  for (int64_t k = static_cast<int64_t>(wave) * 256; k < ld; k += 8 * 256) {
-    const bool in = k + half * 128 < ld;  // the last turn may be half a line: zeros for the other
-    i32x4 fw[4], fx[MT][4];
-    int sw = 0, sx[MT];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) fw[i] = in ? *reinterpret_cast<const i32x4*>(wc + k / 2 + i * 16) : i32x4{0, 0, 0, 0};
-    sw = in ? *reinterpret_cast<const int*>(ws + k / 32) : 0;
-#pragma unroll
-    for (int b = 0; b < MT; ++b) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        fx[b][i] = in ? *reinterpret_cast<const i32x4*>(xc[b] + k / 2 + i * 16) : i32x4{0, 0, 0, 0};
-      sx[b] = in ? *reinterpret_cast<const int*>(xs[b] + k / 32) : 0;
-    }
-#pragma unroll
-    for (int b = 0; b < MT; ++b)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[b] = mfma_mx4_32(fw[i], fx[b][i], acc[b], sw, sx[b], i);
-  }
 #pragma unroll
   for (int b = 0; b < MT; ++b) {
     if (b > 0) __syncthreads();
@@ -382,16 +345,167 @@ __global__ __launch_bounds__(512) void mx4_skinny_kernel(Mx4Operand x, Mx4Operan
     __syncthreads();
     // output o of 1024: row m = o / 32, column n = o % 32
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int o = j * 512 + threadIdx.x;
+    for (int j = 0; j < 16 / WAVES; ++j) {
+      const int o = j * 64 * WAVES + threadIdx.x;
       const int n = o & 31, m = o >> 5;
       const int e = (n >> 3) * 4 + (n & 3), l = ((n >> 2) & 1) * 32 + m;
       float s = part[0][e][l];
 #pragma unroll
-      for (int v = 1; v < 8; ++v) s += part[v][e][l];
-      if (b * 32 + m < x.rows && n0 + n < w.rows) store1<OUT>(y + (b * 32 + m) * stride + n0 + n, s);
+      for (int v = 1; v < WAVES; ++v) s += part[v][e][l];
+      if (b * 32 + m < m_rows && n0 + n < n_rows) store1<OUT>(y + (b * 32 + m) * stride + n0 + n, s);
     }
   }
+}
+
+// Up to 32 MT rows of x by 32 NT rows of W a workgroup, both streamed through LDS.
+// A fragment read straight from memory touches 32 lines for 32 bytes of each
+// and is bound by the address units (24 x 8192 x 16384: 23 us); a direct-to-LDS
+// load here is 8 rows' whole 128-byte lines.  Each wave takes every WAVES-th
+// turn of 256 elements and fills two slots of its own, so the loop has no
+// barrier.  A row's 8 pieces of 16 bytes are stored at piece XOR (row / 2 mod 8):
+// the 16 lanes that read one piece of 16 rows in a cycle touch all 64 banks.
+template <int TILES>
+constexpr int kStreamSlot = TILES * (4096 + 256);
+
+template <int OUT, int NT, int MT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void mx4_stream_kernel(Mx4Operand x, Mx4Operand w, int64_t ld,
+                                                               typename Elem<OUT>::type* __restrict__ y, int64_t stride) {
+  constexpr int TILES = NT + MT, SLOT = kStreamSlot<TILES>, LOADS = 5 * TILES;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = lane >> 5, r32 = lane & 31;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 32 * NT;
+  const int64_t cpitch = ld / 2, spitch = ld / 32;
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)smem));
+  uint8_t* mine = smem + wave * 2 * SLOT;
+  const uint32_t lds_mine = lds0 + wave * 2 * SLOT;
+
+  // Tiles from NT on are x's.  Rows past a matrix read its last row; the second half of a
+  // last turn that is half a line reads the first, with x's codes taken as zeros.
+  uint32_t coff[TILES][4], soff[TILES];
+  const uint8_t *cbase[TILES], *sbase[TILES];
+#pragma unroll
+  for (int a = 0; a < TILES; ++a) {
+    const int64_t first = a < NT ? n0 + a * 32 : (a - NT) * 32, rows = a < NT ? w.rows : x.rows;
+    const int64_t base = first < rows ? first : rows - 1;
+    const int64_t left = rows - base;
+    cbase[a] = (a < NT ? w.codes : x.codes) + base * cpitch;
+    sbase[a] = (a < NT ? w.scales : x.scales) + base * spitch;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = j * 8 + (lane >> 3);
+      coff[a][j] = static_cast<uint32_t>((r < left ? r : left - 1) * cpitch) + (((lane & 7) ^ ((r >> 1) & 7)) * 16);
+    }
+    soff[a] = static_cast<uint32_t>((r32 < left ? r32 : left - 1) * spitch) + half * 4;
+  }
+  auto load_turn = [&](int64_t k, int slot) {
+    const bool partial = k + 128 >= ld;
+    const uint32_t to = lds_mine + slot * SLOT;
+#pragma unroll
+    for (int a = 0; a < TILES; ++a) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // pieces 4 ... 7 are the second half
+        const int piece = (lane & 7) ^ ((((lane >> 3) + j * 8) >> 1) & 7);
+        const uint32_t off = partial && piece >= 4 ? coff[a][j] - 64 : coff[a][j];
+        load_lds16(to + a * 4096 + j * 1024, cbase[a] + k / 2, off);
+      }
+      load_lds4(to + TILES * 4096 + a * 256, sbase[a] + k / 32, partial && half ? soff[a] - 4 : soff[a]);
+    }
+  };
+
+  f32x16 acc[NT][MT];
+#pragma unroll
+  for (int a = 0; a < NT; ++a)
+#pragma unroll
+    for (int b = 0; b < MT; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[a][b][e] = 0.f;
+  const int sw = (r32 >> 1) & 7;
+  constexpr int64_t TURN = WAVES * 256;
+  const int64_t k0 = static_cast<int64_t>(wave) * 256;
+  if (k0 < ld) load_turn(k0, 0);
+  if (k0 + TURN < ld) load_turn(k0 + TURN, 1);
+  int slot = 0;
+  for (int64_t k = k0; k < ld; k += TURN) {
+    if (k + TURN < ld)
+      wait_vm<LOADS>();
+    else
+      wait_vm<0>();
+    const uint8_t* s = mine + slot * SLOT;
+    const bool zero = half && k + 128 >= ld;
+    i32x4 f[TILES][4];
+    int sc[TILES];
+#pragma unroll
+    for (int a = 0; a < TILES; ++a) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        f[a][i] = *reinterpret_cast<const i32x4*>(s + a * 4096 + r32 * 128 + (((half * 4 + i) ^ sw) * 16));
+      sc[a] = *reinterpret_cast<const int*>(s + TILES * 4096 + a * 256 + lane * 4);
+    }
+    wait_lgkm0();
+    if (k + 2 * TURN < ld) load_turn(k + 2 * TURN, slot);
+    if (zero) {
+      // a scale byte of 0 is no NaN, so the products are zeros
+#pragma unroll
+      for (int b = 0; b < MT; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[NT + b][i] = i32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int a = 0; a < TILES; ++a) sc[a] = 0;
+    }
+#pragma unroll
+    for (int a = 0; a < NT; ++a)
+#pragma unroll
+      for (int b = 0; b < MT; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[a][b] = mfma_mx4_32(f[a][i], f[NT + b][i], acc[a][b], sc[a], sc[NT + b], i);
+    slot ^= 1;
+  }
+  __syncthreads();  // the slots become the waves' sums
+  auto part = reinterpret_cast<float(*)[16][64]>(smem);
+#pragma unroll
+  for (int a = 0; a < NT; ++a) {
+    if (a > 0) __syncthreads();
+    join_waves<OUT, MT, WAVES>(acc[a], part, y, stride, n0 + a * 32, x.rows, w.rows);
+  }
+}
+
+// Up to 32 rows of x, quantised here: one launch where the work is small.  An instruction's lane holds a block of 32 elements of one row of x, so
+// the block's max is the lane's own.  A wave's turn is 64 elements.
+template <int TY, int OUT>
+__global__ __launch_bounds__(512) void mx4_fused_kernel(const typename Elem<TY>::type* __restrict__ x, int64_t m, int64_t k,
+                                                       int64_t x_stride, Mx4Operand w, int64_t ld,
+                                                       typename Elem<OUT>::type* __restrict__ y, int64_t stride) {
+  __shared__ float part[8][16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int half = lane >> 5, r32 = lane & 31;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 32;
+  const int64_t wr = n0 + r32 < w.rows ? n0 + r32 : w.rows - 1;
+  const uint8_t* wc = w.codes + wr * (ld / 2) + half * 16;
+  const uint8_t* ws = w.scales + wr * (ld / 32) + half;
+  const auto* xr = x + (r32 < m ? r32 : m - 1) * x_stride;
+  f32x16 acc[1];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) acc[0][e] = 0.f;
+  for (int64_t at = static_cast<int64_t>(wave) * 64; at < k; at += 8 * 64) {
+    const i32x4 fw = *reinterpret_cast<const i32x4*>(wc + at / 2);
+    const int sw = ws[at / 32];
+    const int64_t c = at + half * 32;
+    float v[4][8];
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load8<TY>(xr, c + j * 8, k, v[j]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = max_u32(top, amax_bits(v[j]));
+    const uint32_t byte = scale_byte<kMx4>(top);
+    i32x4 fx;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) fx[j] = static_cast<int>(encode_mx4(v[j], byte));
+    acc[0] = mfma_mx4_32(fw, fx, acc[0], sw, static_cast<int>(byte), 0);
+  }
+  join_waves<OUT, 1, 8>(acc, part, y, stride, n0, m, w.rows);
 }
 
 typedef float f32x4_acc __attribute__((ext_vector_type(4)));

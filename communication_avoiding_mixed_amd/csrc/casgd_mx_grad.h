@@ -49,8 +49,8 @@ constexpr int grad_lds_bytes() {
 // A matrix whose rows are the summed index is staged as it lies, 32 rows of
 // the tile's columns, and transposed by the LDS read (ds_read_b64_tr_b16: 16
 // lanes read four rows of 16 columns, a lane gets its column's four values).
-// Those four rows' 32 bytes would meet in the same banks, so row t's 16-byte
-// pieces are stored at piece XOR 2 (t mod 4).  A matrix whose rows are the
+// The four rows' 64 bytes that 32 lanes read in a cycle would meet in the same
+// banks, so row t's 16-byte pieces are stored at piece XOR 4 (t mod 4).  A matrix whose rows are the
 // output is staged as 64 bytes of each row, as the 4-bit product's codes are.
 template <int OUT, bool ACROSS, int RX, int RC, int GM, int GN>
 __global__ __launch_bounds__(64 * GM * GN, 2) void mx_grad_kernel(GradArgs g, typename Elem<OUT>::type* __restrict__ out_,
@@ -84,7 +84,7 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void mx_grad_kernel(GradArgs g, ty
       const int per_row = is_c ? RC / 8 : RX / 8;
       const int slot = l * 64 + lane;
       const int t = slot / per_row;
-      int p = (slot - t * per_row) ^ ((t & 3) << 1);
+      int p = (slot - t * per_row) ^ ((t & 3) << 2);
       row_in[i] = t;
       piece_in[i] = p;
       const int64_t width = is_c ? g.ld - j0 : g.rows - i0;
@@ -92,7 +92,7 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void mx_grad_kernel(GradArgs g, ty
       off[i] = static_cast<uint32_t>(t * (is_c ? g.ld : g.x_stride) * 2) + p * 16;
     } else {
       int r = l * 16 + (lane >> 2);
-      const int p = (lane & 3) ^ ((r >> 1) & 3);
+      const int p = (lane & 3) ^ ((r >> 2) & 3);
       if (r >= g.rows - i0) r = static_cast<int>(g.rows - i0) - 1;
       row_in[i] = r;
       piece_in[i] = p;
@@ -149,14 +149,19 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void mx_grad_kernel(GradArgs g, ty
   const int half = lane >> 5, r32 = lane & 31;
   // transposed read: row (lane % 16) / 4 of four, columns 16 (lane / 16 % 2) + 4 (lane % 4)
   const int trow = 8 * half + ((lane & 15) >> 2);
-  const int tlow = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1), tx = ((lane & 15) >> 2) << 1;
-  const int tbyte = (lane & 1) * 8;
-  const int teven = (tlow ^ tx) * 16 + tbyte, todd = ((4 + tlow) ^ tx) * 16 + tbyte;
-  const int sw = (r32 >> 1) & 3;
+  const int tq = (lane & 15) >> 2, tlow = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1), tbyte = (lane & 1) * 8;
+  const int sw = (r32 >> 2) & 3;
+  // byte offset in a staged row of tile `a` (32 columns from column 32 a)
+  auto across_offset = [&](int a) { return ((a ^ tq) * 4 + tlow) * 16 + tbyte; };
+  int ocol[WC], orow[WM];
+#pragma unroll
+  for (int a = 0; a < WC; ++a) ocol[a] = trow * RC * 2 + across_offset(wn * WC + a);
+#pragma unroll
+  for (int b = 0; b < WM; ++b)
+    orow[b] = XBASE + (ACROSS ? trow * RX * 2 + across_offset(wm * WM + b) : ((wm * WM + b) * 32 + r32) * 64);
+  const int opiece[2] = {(half ^ sw) * 16, ((2 + half) ^ sw) * 16};
 
-  // tile `a` (32 columns from column 32 a) of a staged matrix `width` columns wide
-  auto read_across = [&](const uint8_t* s, int width, int a, int which) -> bf16x8 {
-    const uint8_t* p = s + (which * 16 + trow) * width * 2 + (a >> 1) * 128 + ((a & 1) ? todd : teven);
+  auto read_across = [&](const uint8_t* p, int width) -> bf16x8 {
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
     const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * width * 2));
     const __attribute__((ext_vector_type(8))) short v = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
@@ -175,14 +180,13 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void mx_grad_kernel(GradArgs g, ty
   auto read_frags = [&](int which, int st) {
     const uint8_t* s = smem + (st & 3) * STAGE;
 #pragma unroll
-    for (int a = 0; a < WC; ++a) fc[which][a] = read_across(s, RC, wn * WC + a, which);
+    for (int a = 0; a < WC; ++a) fc[which][a] = read_across(s + ocol[a] + which * 16 * RC * 2, RC);
 #pragma unroll
     for (int b = 0; b < WM; ++b) {
       if constexpr (ACROSS)
-        fx[which][b] = read_across(s + XBASE, RX, wm * WM + b, which);
+        fx[which][b] = read_across(s + orow[b] + which * 16 * RX * 2, RX);
       else
-        fx[which][b] = *reinterpret_cast<const bf16x8*>(s + XBASE + ((wm * WM + b) * 32 + r32) * 64 +
-                                                       (((2 * which + half) ^ sw) * 16));
+        fx[which][b] = *reinterpret_cast<const bf16x8*>(s + orow[b] + opiece[which]);
     }
   };
 

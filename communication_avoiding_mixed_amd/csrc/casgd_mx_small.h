@@ -1,0 +1,309 @@
+// Gradients of the low-precision layer where the work is too small for the
+// tiled form's extra launches: one launch that reads dy and the codes as they
+// are.
+//
+// A wave owns a 64 x 64 tile of the output and every D-th slice of 32 of the
+// summed index; it widens its slice of the codes (and of dy, where dy's rows
+// are the summed index) to bf16 in LDS of its own and reads fragments from
+// there, so the loop has no barrier.  The D waves of a tile then add their
+// sums in a fixed order.  Bound by latency: the next slice's loads are in
+// flight while one is computed.
+#pragma once
+
+#include <type_traits>
+
+#include "casgd_mx_grad.h"
+
+namespace casgd {
+namespace mx {
+
+// The high halves of two words, a's below b's.
+__device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
+
+// v[0 .. 7] as PARTS bf16 vectors that sum to it exactly: each keeps the 8
+// leading bits of what is left, cut towards zero so that none overflows; a
+// value that is not finite is its first part.  Vectors with such a value take
+// a branch of their own.
+template <int PARTS>
+__device__ __forceinline__ void split8(float v[8], u32x4 (&out)[PARTS]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max_u32(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  if (top >= 0x7F800000u) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t bits = __float_as_uint(v[i]);
+      const bool nan = (bits & 0x7FFFFFFFu) > 0x7F800000u, inf = (bits & 0x7FFFFFFFu) == 0x7F800000u;
+      // a NaN keeps a set fraction bit among the 7 that stay
+      const uint32_t word = nan ? bits | 0x400000u : bits;
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p) {
+        const uint32_t left = p == 0 ? word : __float_as_uint(v[i]);
+        out[p][i / 2] = (i & 1) ? high_halves(out[p][i / 2] << 16, left) : left >> 16;
+        v[i] = nan || inf ? 0.f : v[i] - __uint_as_float(left & 0xFFFF0000u);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int p = 0; p < PARTS; ++p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[p][i] = high_halves(__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1]));
+    if (p + 1 < PARTS)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] -= __uint_as_float(__float_as_uint(v[i]) & 0xFFFF0000u);
+  }
+}
+
+template <int TY>
+constexpr int kParts = TY == kBF16 ? 1 : TY == kF16 ? 2 : 3;
+
+// 32 codes of one block to bf16
+__device__ __forceinline__ void widen_block4(u32x4 w, float scale, u32x4 out[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    out[i].x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i], scale, 0));
+    out[i].y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i], scale, 1));
+    out[i].z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i], scale, 2));
+    out[i].w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i], scale, 3));
+  }
+}
+__device__ __forceinline__ void widen_block8(u32x4 a, u32x4 b, float scale, u32x4 out[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const u32x4 w = i < 2 ? a : b;
+    const int k = (i & 1) * 2;
+    out[i].x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[k], scale, false));
+    out[i].y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[k], scale, true));
+    out[i].z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[k + 1], scale, false));
+    out[i].w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[k + 1], scale, true));
+  }
+}
+
+struct SmallArgs {
+  int64_t x_stride, x_cols;  // dy as it lies; x_cols: its columns
+  int64_t rows, cols, depth; // out (rows x cols) = sum over depth
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int64_t ld;
+  uint32_t tiles_c, tiles;
+  int slices, ways;          // ways: D, a power of two up to 8
+  int region;                // LDS bytes of a wave
+};
+
+template <int TY, bool ACROSS>
+constexpr int small_region(int ways) {
+  const int stage = 4096 * (1 + (ACROSS ? kParts<TY> : 0));
+  return ways > 1 && stage < 16384 ? 16384 : stage;  // a wave's 64 x 64 sums
+}
+
+template <int TY, bool ACROSS, int OUT>
+__global__ __launch_bounds__(512) void mx_small_grad_kernel(SmallArgs g, const typename Elem<TY>::type* __restrict__ x,
+                                                           typename Elem<OUT>::type* __restrict__ out, int64_t stride,
+                                                           int accumulate) {
+  constexpr int PARTS = kParts<TY>;
+  constexpr int FMT = ACROSS ? kMx8 : kMx4;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int part = wave & (g.ways - 1);
+  const uint32_t tile = blockIdx.x * (8 / g.ways) + wave / g.ways;
+  const bool live = tile < g.tiles;
+  const int64_t i0 = live ? static_cast<int64_t>(tile / g.tiles_c) * 64 : 0;
+  const int64_t j0 = live ? static_cast<int64_t>(tile % g.tiles_c) * 64 : 0;
+  uint8_t* mine = smem + wave * g.region;
+  const int half = lane >> 5, r32 = lane & 31;
+
+  // staging: two lanes a row of the slice, 32 elements (one block) each
+  const int srow = lane >> 1, shalf = lane & 1;
+  constexpr int NW = FMT == kMx8 ? 2 : 1;
+  constexpr int XW = TY == kF32 ? 2 : 1;
+  auto fetch = [&](int s, u32x4 (&c)[NW], float& scale, u32x4 (&xw)[4][XW]) {
+    const int64_t t = static_cast<int64_t>(s) * 32 + srow;
+    const bool in = t < g.depth;
+    const u32x4 zero = {0u, 0u, 0u, 0u};
+    const int64_t at = t * g.ld + j0 + shalf * 32;  // in elements
+    if constexpr (FMT == kMx8) {
+      c[0] = in ? *reinterpret_cast<const u32x4*>(g.codes + at) : zero;
+      c[1] = in ? *reinterpret_cast<const u32x4*>(g.codes + at + 16) : zero;
+    } else {
+      c[0] = in ? *reinterpret_cast<const u32x4*>(g.codes + at / 2) : zero;
+    }
+    scale = in ? scale_value(g.scales[at >> 5]) : 1.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // across: 8 columns of row t; along: fragment i (row tile i / 2, half-slice i % 2)
+      const int64_t row = ACROSS ? t : i0 + (i >> 1) * 32 + r32;
+      const int64_t col = ACROSS ? i0 + shalf * 32 + i * 8 : static_cast<int64_t>(s) * 32 + (i & 1) * 16 + half * 8;
+      const bool ok = row < (ACROSS ? g.depth : g.rows);
+      const auto* p = x + row * g.x_stride + col;
+#pragma unroll
+      for (int h = 0; h < XW; ++h) xw[i][h] = zero;
+      if (ok && col + 8 <= g.x_cols) {
+#pragma unroll
+        for (int h = 0; h < XW; ++h) xw[i][h] = *reinterpret_cast<const u32x4_any*>(p + 4 * h);
+      } else if (ok) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t bits = col + e < g.x_cols ? __builtin_bit_cast(
+              typename std::conditional<TY == kF32, uint32_t, uint16_t>::type, p[e]) : 0u;
+          if constexpr (TY == kF32)
+            xw[i][e / 4][e & 3] = bits;
+          else
+            xw[i][0][e / 2] |= bits << (16 * (e & 1));
+        }
+      }
+    }
+  };
+  auto parts_of_raw = [&](const u32x4 (&r)[XW], u32x4 (&w)[PARTS]) {
+    if constexpr (TY == kBF16) {
+      w[0] = r[0];
+    } else {
+      Raw8<TY> raw;
+#pragma unroll
+      for (int h = 0; h < XW; ++h) raw.w[h] = r[h];
+      float v[8];
+      widen8<TY>(raw, v);
+      split8<PARTS>(v, w);
+    }
+  };
+
+  // 16-byte piece p of staged row t lies at piece p XOR 4 (t / 2 mod 2): the 32
+  // lanes of a transposed read's cycle take 64 bytes of four rows of 128 bytes
+  const int sx = ((srow >> 1) & 1) << 2;
+  const int trow = 8 * half + ((lane & 15) >> 2);
+  const int tlow = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1), tx = ((lane & 15) >> 3) << 2;
+  const int tbyte = (lane & 1) * 8;
+  auto read_across = [&](const uint8_t* s, int a, int which) -> bf16x8 {
+    const uint8_t* p = s + (which * 16 + trow) * 128 + ((a * 4 + tlow) ^ tx) * 16 + tbyte;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * 128));
+    const __attribute__((ext_vector_type(8))) short v = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    return __builtin_bit_cast(bf16x8, v);
+  };
+
+  f32x16 acc[2][2];
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[a][b][e] = 0.f;
+
+  if (live && part < g.slices) {
+    auto compute = [&](const u32x4 (&cc)[NW], float cscale, const u32x4 (&cx)[4][XW]) {
+      u32x4 w[4];
+      if constexpr (FMT == kMx8)
+        widen_block8(cc[0], cc[1], cscale, w);
+      else
+        widen_block4(cc[0], cscale, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4*>(mine + srow * 128 + (((shalf * 4 + i) ^ sx) * 16)) = w[i];
+      bf16x8 fx[2][2][PARTS];  // [row tile][half-slice][part]
+      if constexpr (ACROSS) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          u32x4 q[PARTS];
+          parts_of_raw(cx[i], q);
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p)
+            *reinterpret_cast<u32x4*>(mine + 4096 * (1 + p) + srow * 128 + (((shalf * 4 + i) ^ sx) * 16)) = q[p];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          u32x4 q[PARTS];
+          parts_of_raw(cx[i], q);
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) fx[i >> 1][i & 1][p] = __builtin_bit_cast(bf16x8, q[p]);
+        }
+      }
+      // the wave's own LDS: its accesses are carried out in order
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        bf16x8 fc[2];
+#pragma unroll
+        for (int a = 0; a < 2; ++a) fc[a] = read_across(mine, a, k);
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) {
+            bf16x8 f;
+            if constexpr (ACROSS)
+              f = read_across(mine + 4096 * (1 + p), b, k);
+            else
+              f = fx[b][k][p];
+#pragma unroll
+            for (int a = 0; a < 2; ++a) acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fc[a], f, acc[a][b], 0, 0, 0);
+          }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    };
+    // two slices in flight; one past the end is zeros, its rows being past the
+    // summed index
+    u32x4 c0[NW], c1[NW], x0[4][XW], x1[4][XW];
+    float s0, s1;
+    fetch(part, c0, s0, x0);
+    fetch(part + g.ways, c1, s1, x1);
+    for (int s = part; s < g.slices; s += 2 * g.ways) {
+      compute(c0, s0, x0);
+      fetch(s + 2 * g.ways, c0, s0, x0);
+      compute(c1, s1, x1);
+      fetch(s + 3 * g.ways, c1, s1, x1);
+    }
+  }
+
+  // Sums of 4 neighbouring columns at a time: group q of 16 is acc[q / 8][q / 4 % 2][4 (q % 4) ...]
+  auto store = [&](int q, f32x4 v) {
+    const int a = q >> 3, b = (q >> 2) & 1;
+    const int64_t i = i0 + b * 32 + r32, j = j0 + a * 32 + (q & 3) * 8 + half * 4;
+    if (!live || i >= g.rows) return;
+    auto* p = out + i * stride + j;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (accumulate && j + e < g.cols) v[e] += load1<OUT>(p + e);
+    if (j + 4 <= g.cols) {
+      if constexpr (OUT == kF32)
+        *reinterpret_cast<u32x4_any*>(p) = __builtin_bit_cast(u32x4, v);
+      else
+        *reinterpret_cast<u32x2_any*>(p) = u32x2{narrow2<OUT>(v.x, v.y), narrow2<OUT>(v.z, v.w)};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (j + e < g.cols) store1<OUT>(p + e, v[e]);
+    }
+  };
+  if (g.ways == 1) {
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      const f32x16& c = acc[q >> 3][(q >> 2) & 1];
+      const int e = 4 * (q & 3);
+      store(q, f32x4{c[e], c[e + 1], c[e + 2], c[e + 3]});
+    }
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    const f32x16& c = acc[q >> 3][(q >> 2) & 1];
+    const int e = 4 * (q & 3);
+    *reinterpret_cast<f32x4*>(mine + (q * 64 + lane) * 16) = f32x4{c[e], c[e + 1], c[e + 2], c[e + 3]};
+  }
+  __syncthreads();
+  const uint8_t* group = smem + (wave - part) * g.region;
+  const int per = 16 / g.ways;
+  for (int q = part * per; q < (part + 1) * per; ++q) {
+    f32x4 v = *reinterpret_cast<const f32x4*>(group + (q * 64 + lane) * 16);
+    for (int d = 1; d < g.ways; ++d) {
+      const f32x4 u = *reinterpret_cast<const f32x4*>(group + d * g.region + (q * 64 + lane) * 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += u[e];
+    }
+    store(q, v);
+  }
+}
+
+}  // namespace mx
+}  // namespace casgd

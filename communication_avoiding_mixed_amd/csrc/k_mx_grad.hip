@@ -9,6 +9,7 @@
 #include "casgd.h"
 #include "casgd_internal.h"
 #include "casgd_mx_grad.h"
+#include "casgd_mx_small.h"
 
 namespace casgd {
 namespace mx {
@@ -38,8 +39,7 @@ __global__ __launch_bounds__(kThreads) void mx_widen_kernel(const uint8_t* __res
 }
 
 // dy (rows x cols) as PARTS bf16 matrices [rows_pad][pitch], zeros in the
-// padding.  Each part keeps the 8 leading bits of what is left, cut towards
-// zero so that no part overflows; a value that is not finite is its first part.
+// padding.
 template <int TY, int PARTS>
 __global__ __launch_bounds__(kThreads) void split_kernel(const typename Elem<TY>::type* __restrict__ dy, int64_t rows,
                                                         int64_t cols, int64_t stride, int64_t rows_pad, int64_t pitch,
@@ -50,23 +50,10 @@ __global__ __launch_bounds__(kThreads) void split_kernel(const typename Elem<TY>
     const int64_t r = at / per_row, c = (at - r * per_row) * 8;
     float v[8] = {};
     if (r < rows) load8<TY>(dy + r * stride, c, cols, v);
+    u32x4 w[PARTS];
+    split8<PARTS>(v, w);
 #pragma unroll
-    for (int p = 0; p < PARTS; ++p) {
-      u32x4 w;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t bits = __float_as_uint(v[i]);
-        const bool fine = (bits & 0x7F800000u) != 0x7F800000u;
-        // a NaN keeps a set fraction bit among the 7 that stay
-        const uint32_t top = fine ? bits >> 16 : (bits >> 16) | ((bits & 0x7FFFFFu) ? 0x40u : 0u);
-        if (i & 1)
-          w[i / 2] |= top << 16;
-        else
-          w[i / 2] = top;
-        v[i] = fine ? v[i] - __uint_as_float(bits & 0xFFFF0000u) : 0.f;
-      }
-      reinterpret_cast<u32x4*>(out)[p * chunks + at] = w;
-    }
+    for (int p = 0; p < PARTS; ++p) reinterpret_cast<u32x4*>(out)[p * chunks + at] = w[p];
   }
 }
 
@@ -110,6 +97,9 @@ struct Plan {
   bool across;
   int parts, stages, splits, per_split, tile;
   bool copy;
+  bool small;            // the one-launch form: 64 x 64 tiles, `ways` waves each
+  int64_t tiles64;
+  int ways;
   int64_t pitch, x_pad;  // of the copy
   int64_t c_bytes, x_bytes, s_bytes;
 };
@@ -128,6 +118,25 @@ Plan plan_of(bool across, int64_t m, int64_t n, int64_t k, int type, const void*
   p.copy = type != kBF16 || reinterpret_cast<uintptr_t>(dy) % 16 != 0 || stride % 8 != 0 || stride > (int64_t{1} << 22);
   p.pitch = up(n, 32);
   p.x_pad = across ? up(m, 32) : m;
+  // The one-launch form: as many waves share a tile's summed index as fill the
+  // CUs with 8 waves each, while every wave has a slice.  Against the tiled
+  // form (widening, copying and adding up in launches of their own), rows x n
+  // x k, bf16 / float32 dy, us a call, dx and dW:
+  //   37 x 1000 x 2000    11 / 16 and 11 / 13   (tiled 16 / 21 and 13 / 17)
+  //   1024 x 1024 x 1024  12 / 20 and 11 / 21   (tiled 22 / 31 and 22 / 32)
+  //   2048 x 2048 x 1024  29 / 57 and 28 / 55   (tiled 31 / 68 and 33 / 68)
+  //   64 x 4096 x 4096    33 / 54               (tiled 30 / 47: 16 slices a wave on 64 CUs)
+  //   4096 x 512 x 512    dW 28 / 55            (tiled 21 / 33: 16 slices a wave on 64 CUs)
+  // so it is taken up to this work while a wave has few slices or the CUs are full.
+  p.tiles64 = ((p.rows + 63) / 64) * ((p.cols + 63) / 64);
+  p.ways = 1;
+  while (p.ways < 8 && p.tiles64 * p.ways < 2048 && p.stages > p.ways) p.ways *= 2;
+  p.small = static_cast<double>(p.depth) * p.rows * p.cols <= 4.5e9 &&
+            (p.stages <= 8 * p.ways || p.tiles64 * p.ways >= 2048);
+  if (p.small) {
+    p.c_bytes = p.x_bytes = p.s_bytes = 0;
+    return p;
+  }
   p.c_bytes = up(static_cast<int64_t>(p.stages) * 32 * p.ld * 2, 256);
   p.x_bytes = p.copy ? up(p.parts * p.x_pad * p.pitch * 2, 256) : 0;
   // 256 x 256 tiles where there are enough for most of the 256 CUs; with
@@ -195,9 +204,53 @@ hipError_t grad_to(int type, const GradArgs& g, const Plan& p, void* out, int64_
   return grad_as<kF32, ACROSS>(g, p, out, stride, 0, accumulate, stream);
 }
 
+template <int TY, bool ACROSS, int OUT>
+hipError_t small_as(const Plan& p, const void* dy, int64_t dy_stride, const uint8_t* codes, const uint8_t* scales, void* out,
+                    int64_t stride, int accumulate, hipStream_t stream) {
+  auto* kernel = mx_small_grad_kernel<TY, ACROSS, OUT>;
+  constexpr int most = 8 * small_region<TY, ACROSS>(8);
+  static const hipError_t allowed =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (allowed != hipSuccess) return allowed;
+  SmallArgs g = {};
+  g.x_stride = dy_stride;
+  g.x_cols = p.x_cols;
+  g.rows = p.rows;
+  g.cols = p.cols;
+  g.depth = p.depth;
+  g.codes = codes;
+  g.scales = scales;
+  g.ld = p.ld;
+  g.tiles_c = static_cast<uint32_t>((p.cols + 63) / 64);
+  g.tiles = static_cast<uint32_t>(p.tiles64);
+  g.slices = p.stages;
+  g.ways = p.ways;
+  g.region = small_region<TY, ACROSS>(g.ways);
+  const uint32_t per = 8 / g.ways;
+  hipLaunchKernelGGL(kernel, dim3((g.tiles + per - 1) / per), dim3(512), 8 * g.region, stream, g,
+                     static_cast<const typename Elem<TY>::type*>(dy), static_cast<typename Elem<OUT>::type*>(out), stride,
+                     accumulate);
+  return hipGetLastError();
+}
+
+template <bool ACROSS, int TY>
+hipError_t small_to(const Plan& p, const void* dy, int64_t dy_stride, const uint8_t* codes, const uint8_t* scales, void* out,
+                    int type, int64_t stride, int accumulate, hipStream_t stream) {
+  if (type == kBF16) return small_as<TY, ACROSS, kBF16>(p, dy, dy_stride, codes, scales, out, stride, accumulate, stream);
+  if (type == kF16) return small_as<TY, ACROSS, kF16>(p, dy, dy_stride, codes, scales, out, stride, accumulate, stream);
+  return small_as<TY, ACROSS, kF32>(p, dy, dy_stride, codes, scales, out, stride, accumulate, stream);
+}
+
 template <bool ACROSS, int FMT>
 hipError_t run_grad(const Plan& p, const void* dy, int type, int64_t dy_stride, const uint8_t* codes, const uint8_t* scales,
                     void* out, int out_type, int64_t stride, int accumulate, uint8_t* workspace, hipStream_t stream) {
+  if (p.small) {
+    if (type == kBF16)
+      return small_to<ACROSS, kBF16>(p, dy, dy_stride, codes, scales, out, out_type, stride, accumulate, stream);
+    if (type == kF16)
+      return small_to<ACROSS, kF16>(p, dy, dy_stride, codes, scales, out, out_type, stride, accumulate, stream);
+    return small_to<ACROSS, kF32>(p, dy, dy_stride, codes, scales, out, out_type, stride, accumulate, stream);
+  }
   uint16_t* c = reinterpret_cast<uint16_t*>(workspace);
   uint16_t* x = reinterpret_cast<uint16_t*>(workspace + p.c_bytes);
   float* sums = reinterpret_cast<float*>(workspace + p.c_bytes + p.x_bytes);
@@ -269,8 +322,8 @@ int casgd_mx4_grad_input(const void* dy, int dy_type, int64_t m, int64_t n, int6
   if (const char* why = mx::bad_codes(w_codes, w_scales, n, mx::kMx4)) return api_fail(CASGD_EINVAL, why);
   if (const char* why = mx::bad_grad(m, n, k)) return api_fail(CASGD_EINVAL, why);
   if (m == 0) return CASGD_OK;
-  if (!dy || !dx || !workspace) return api_fail(CASGD_EINVAL, "NULL pointer");
   const mx::Plan p = mx::plan_of(false, m, n, k, dy_type, dy, dy_stride);
+  if (!dy || !dx || (!p.small && !workspace)) return api_fail(CASGD_EINVAL, "NULL pointer");
   if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return api_fail(CASGD_EINVAL, "workspace must be 256-byte aligned");
   if (workspace_bytes < p.c_bytes + p.x_bytes + p.s_bytes) return api_fail(CASGD_EINVAL, "workspace too small");
   const hipError_t e = mx::run_grad<false, mx::kMx4>(p, dy, dy_type, dy_stride, w_codes, w_scales, dx, dx_type, dx_stride, 0,
@@ -285,8 +338,8 @@ int casgd_mx8_grad_weight(const void* dy, int dy_type, int64_t t, int64_t n, int
   if (const char* why = mx::bad_matrix(n, k, dw_stride, dw_type)) return api_fail(CASGD_EINVAL, why);
   if (const char* why = mx::bad_codes(x_codes, x_scales, t, mx::kMx8)) return api_fail(CASGD_EINVAL, why);
   if (const char* why = mx::bad_grad(t, n, k)) return api_fail(CASGD_EINVAL, why);
-  if (!dw || (t > 0 && (!dy || !workspace))) return api_fail(CASGD_EINVAL, "NULL pointer");
   const mx::Plan p = mx::plan_of(true, t, n, k, dy_type, dy, dy_stride);
+  if (!dw || (t > 0 && (!dy || (!p.small && !workspace)))) return api_fail(CASGD_EINVAL, "NULL pointer");
   if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return api_fail(CASGD_EINVAL, "workspace must be 256-byte aligned");
   if (workspace_bytes < p.c_bytes + p.x_bytes + p.s_bytes) return api_fail(CASGD_EINVAL, "workspace too small");
   hipStream_t stream = static_cast<hipStream_t>(hip_stream);

@@ -8,12 +8,16 @@ namespace casgd {
 namespace mx {
 namespace {
 
-constexpr int kSkinnyRows = 128;
 constexpr int64_t kMaxDepth = int64_t{1} << 24;  // 256 rows of codes stay below 2^32 bytes
 
-// Rows of x up to which quantising them again in every workgroup costs less
-// than a launch of its own
-bool decodes(int64_t m, int64_t k, int64_t n) { return m <= 16 && n * k <= (int64_t{1} << 25); }
+// The one-launch forms quantise x again in every workgroup, which costs less
+// than a launch of its own where a wave's share of it is small.
+//   16 rows a workgroup:  16 x 4096 x 4096 11.5 us (two launches 12.7),
+//                         16 x 8192 x 4096 21 us (two launches 13)
+//   32 rows a workgroup:  20 x 512 x 512 8.2 us (12.8), 20 x 2048 x 2048 9.1 us
+//                         (13.1), 32 x 4096 x 4096 16.5 us (12.7)
+bool decodes(int64_t m, int64_t k, int64_t n) { return m <= 16 && n * k <= (int64_t{1} << 24); }
+bool fuses(int64_t m, int64_t k, int64_t n) { return m <= 32 && (k + 511) / 512 * ((n + 8191) / 8192) <= 4; }
 
 template <int OUT, int RX, int RW, int GM, int GN>
 hipError_t gemm_as(const Mx4Operand& x, const Mx4Operand& w, int64_t ld, void* y, int64_t stride, hipStream_t stream) {
@@ -29,21 +33,32 @@ hipError_t gemm_as(const Mx4Operand& x, const Mx4Operand& w, int64_t ld, void* y
   return hipGetLastError();
 }
 
+template <int OUT, int NT, int MT, int WAVES>
+hipError_t stream_as(const Mx4Operand& x, const Mx4Operand& w, int64_t ld, typename Elem<OUT>::type* y, int64_t stride,
+                     hipStream_t stream) {
+  constexpr int lds = WAVES * 2 * kStreamSlot<NT + MT>;
+  auto* kernel = mx4_stream_kernel<OUT, NT, MT, WAVES>;
+  static const hipError_t allowed =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (allowed != hipSuccess) return allowed;
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>((w.rows + 32 * NT - 1) / (32 * NT))), dim3(64 * WAVES), lds, stream, x,
+                     w, ld, y, stride);
+  return hipGetLastError();
+}
+
 template <int OUT>
 hipError_t product_as(const Mx4Operand& x, const Mx4Operand& w, int64_t ld, void* y, int64_t stride, hipStream_t stream) {
   auto* out = static_cast<typename Elem<OUT>::type*>(y);
-  const dim3 grid(static_cast<unsigned>((w.rows + 31) / 32)), block(512);
+  // few rows: bound by streaming W, whose rows go 64 to a workgroup where that
+  // still gives most CUs one
+  const bool wide = w.rows >= 64 * 192;
   if (x.rows <= 32)
-    hipLaunchKernelGGL((mx4_skinny_kernel<OUT, 1>), grid, block, 0, stream, x, w, ld, out, stride);
-  else if (x.rows <= 64)
-    hipLaunchKernelGGL((mx4_skinny_kernel<OUT, 2>), grid, block, 0, stream, x, w, ld, out, stride);
-  else if (x.rows <= kSkinnyRows)
-    hipLaunchKernelGGL((mx4_skinny_kernel<OUT, 4>), grid, block, 0, stream, x, w, ld, out, stride);
-  else if (((x.rows + 255) / 256) * ((w.rows + 255) / 256) >= 256)
-    return gemm_as<OUT, 256, 256, 4, 2>(x, w, ld, y, stride, stream);
-  else
-    return gemm_as<OUT, 128, 128, 2, 2>(x, w, ld, y, stride, stream);
-  return hipGetLastError();
+    return wide ? stream_as<OUT, 2, 1, 4>(x, w, ld, out, stride, stream) : stream_as<OUT, 1, 1, 8>(x, w, ld, out, stride, stream);
+  if (x.rows <= 64)
+    return wide ? stream_as<OUT, 2, 2, 4>(x, w, ld, out, stride, stream) : stream_as<OUT, 1, 2, 4>(x, w, ld, out, stride, stream);
+  // the large tile moves half the bytes per product; it needs one for every CU
+  if (((x.rows + 255) / 256) * ((w.rows + 255) / 256) >= 256) return gemm_as<OUT, 256, 256, 4, 2>(x, w, ld, y, stride, stream);
+  return gemm_as<OUT, 128, 128, 2, 2>(x, w, ld, y, stride, stream);
 }
 
 hipError_t launch_product(int type, const Mx4Operand& x, const Mx4Operand& w, int64_t ld, void* y, int64_t stride,
@@ -62,12 +77,22 @@ hipError_t decode_as(const void* x, int64_t m, int64_t k, int64_t x_stride, cons
   return hipGetLastError();
 }
 
+template <int TY, int OUT>
+hipError_t one_launch_as(const void* x, int64_t m, int64_t k, int64_t x_stride, const Mx4Operand& w, void* y, int64_t stride,
+                         hipStream_t stream) {
+  if (decodes(m, k, w.rows)) return decode_as<TY, OUT>(x, m, k, x_stride, w, y, stride, stream);
+  hipLaunchKernelGGL((mx4_fused_kernel<TY, OUT>), dim3(static_cast<unsigned>((w.rows + 31) / 32)), dim3(512), 0, stream,
+                     static_cast<const typename Elem<TY>::type*>(x), m, k, x_stride, w, ld_of(k),
+                     static_cast<typename Elem<OUT>::type*>(y), stride);
+  return hipGetLastError();
+}
+
 template <int TY>
-hipError_t decode_from(const void* x, int64_t m, int64_t k, int64_t x_stride, const Mx4Operand& w, void* y, int type,
-                       int64_t stride, hipStream_t stream) {
-  if (type == kBF16) return decode_as<TY, kBF16>(x, m, k, x_stride, w, y, stride, stream);
-  if (type == kF16) return decode_as<TY, kF16>(x, m, k, x_stride, w, y, stride, stream);
-  return decode_as<TY, kF32>(x, m, k, x_stride, w, y, stride, stream);
+hipError_t one_launch(const void* x, int64_t m, int64_t k, int64_t x_stride, const Mx4Operand& w, void* y, int type,
+                      int64_t stride, hipStream_t stream) {
+  if (type == kBF16) return one_launch_as<TY, kBF16>(x, m, k, x_stride, w, y, stride, stream);
+  if (type == kF16) return one_launch_as<TY, kF16>(x, m, k, x_stride, w, y, stride, stream);
+  return one_launch_as<TY, kF32>(x, m, k, x_stride, w, y, stride, stream);
 }
 
 }  // namespace
@@ -80,7 +105,7 @@ extern "C" {
 
 int64_t casgd_mx4_linear_workspace(int64_t m, int64_t k, int64_t n) {
   if (m < 0 || m > mx::kMaxDim || k < 1 || k > mx::kMaxDim || n < 0 || n > mx::kMaxDim) return -1;
-  if (mx::decodes(m, k, n)) return 0;
+  if (mx::decodes(m, k, n) || mx::fuses(m, k, n)) return 0;
   const int64_t ld = mx::ld_of(k);
   return m * (ld / 2 + ld / mx::kBlock);
 }
@@ -103,13 +128,13 @@ int casgd_mx4_linear(const void* x, int x_type, int64_t m, int64_t k, int64_t x_
   uint8_t* scales = codes + m * (ld / 2);
   const mx::Mx4Operand w{w_codes, w_scales, n};
   hipError_t e;
-  if (mx::decodes(m, k, n)) {
+  if (need == 0) {
     if (x_type == mx::kBF16)
-      e = mx::decode_from<mx::kBF16>(x, m, k, x_stride, w, y, y_type, y_stride, stream);
+      e = mx::one_launch<mx::kBF16>(x, m, k, x_stride, w, y, y_type, y_stride, stream);
     else if (x_type == mx::kF16)
-      e = mx::decode_from<mx::kF16>(x, m, k, x_stride, w, y, y_type, y_stride, stream);
+      e = mx::one_launch<mx::kF16>(x, m, k, x_stride, w, y, y_type, y_stride, stream);
     else
-      e = mx::decode_from<mx::kF32>(x, m, k, x_stride, w, y, y_type, y_stride, stream);
+      e = mx::one_launch<mx::kF32>(x, m, k, x_stride, w, y, y_type, y_stride, stream);
   } else {
     e = mx::launch_quantize(mx::kMx4, x_type, x, m, k, x_stride, codes, scales, stream);
     if (e == hipSuccess) e = mx::launch_product(y_type, {codes, scales, m}, w, ld, y, y_stride, stream);

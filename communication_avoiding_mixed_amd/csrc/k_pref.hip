@@ -33,14 +33,26 @@ __device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b) {
   return {m, a.s * exp_hw(a.m - m) + b.s * exp_hw(b.m - m)};
 }
 
-// One workgroup per row.  NaN: v_max drops NaN operands, but exp(NaN - m) in
-// the sum keeps it.
+// 8 logits from column c; -inf past the row's end
 template <int TY>
-__global__ __launch_bounds__(kThreads) void row_stats_kernel(const typename Elem<TY>::type* __restrict__ logits, int64_t vocab,
-                                                            int64_t stride, const int64_t* __restrict__ labels,
-                                                            float* __restrict__ logps, double* __restrict__ logps64,
-                                                            float2* __restrict__ stats) {
-  __shared__ MaxSum part[kWaves];
+__device__ __forceinline__ void load_logits(const typename Elem<TY>::type* row, int64_t c, int64_t vocab, float v[8]) {
+  if (c + 8 <= vocab) {
+    widen8<TY>(load_raw8<TY>(row + c), v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < vocab ? load1<TY>(row + c + i) : -INFINITY;
+  }
+}
+
+// One workgroup per row, four 16-byte loads of a lane in flight.  NaN: the
+// max drops NaN operands, but exp(NaN - m) in the sum keeps it.
+template <int TY, int THREADS>
+__global__ __launch_bounds__(THREADS) void row_stats_kernel(const typename Elem<TY>::type* __restrict__ logits, int64_t vocab,
+                                                           int64_t stride, const int64_t* __restrict__ labels,
+                                                           float* __restrict__ logps, double* __restrict__ logps64,
+                                                           float2* __restrict__ stats) {
+  constexpr int WAVES = THREADS / 64;
+  __shared__ MaxSum part[WAVES];
   const int64_t t = blockIdx.x;
   const int64_t label = labels[t];
   if (label < 0) {
@@ -52,22 +64,36 @@ __global__ __launch_bounds__(kThreads) void row_stats_kernel(const typename Elem
     return;
   }
   const auto* row = logits + t * stride;
+  // a label past the vocabulary is not read: its row becomes NaN
+  const float z = label < vocab ? load1<TY>(row + label) : NAN;
   MaxSum acc = {-INFINITY, 0.f};
-  for (int64_t c = static_cast<int64_t>(threadIdx.x) * 8; c < vocab; c += kThreads * 8) {
-    float v[8];
-    if (c + 8 <= vocab) {
-      widen8<TY>(load_raw8<TY>(row + c), v);
+  constexpr int UNROLL = 4;
+  for (int64_t c = static_cast<int64_t>(threadIdx.x) * 8; c < vocab; c += UNROLL * THREADS * 8) {
+    float v[UNROLL][8];
+    if (c + (UNROLL - 1) * THREADS * 8 + 8 <= vocab) {
+      Raw8<TY> raw[UNROLL];
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) raw[u] = load_raw8<TY>(row + c + u * THREADS * 8);
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) widen8<TY>(raw[u], v[u]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = c + i < vocab ? load1<TY>(row + c + i) : -INFINITY;
+      for (int u = 0; u < UNROLL; ++u) load_logits<TY>(row, c + u * THREADS * 8, vocab, v[u]);
     }
     float m = acc.m;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, v[i]);
+    for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, v[u][i]);
     const float base = m == -INFINITY ? 0.f : m;
     float s = acc.s * exp_hw(acc.m - base);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s += exp_hw(v[i] - base);
+    for (int u = 0; u < UNROLL; ++u) {
+      float part_sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) part_sum += exp_hw(v[u][i] - base);
+      s += part_sum;
+    }
     acc = {m, s};
   }
 #pragma unroll
@@ -76,9 +102,7 @@ __global__ __launch_bounds__(kThreads) void row_stats_kernel(const typename Elem
   __syncthreads();
   if (threadIdx.x != 0) return;
   acc = part[0];
-  for (int w = 1; w < kWaves; ++w) acc = join(acc, part[w]);
-  // a label past the vocabulary is not read: its row becomes NaN
-  const float z = label < vocab ? load1<TY>(row + label) : NAN;
+  for (int w = 1; w < WAVES; ++w) acc = join(acc, part[w]);
   const double lp = (static_cast<double>(z) - acc.m) - log(static_cast<double>(acc.s));
   logps[t] = static_cast<float>(lp);
   if (logps64) logps64[t] = lp;
@@ -87,42 +111,45 @@ __global__ __launch_bounds__(kThreads) void row_stats_kernel(const typename Elem
 
 __device__ __forceinline__ int64_t clamp_row(int64_t r, int64_t tokens) { return r < 0 ? 0 : r > tokens ? tokens : r; }
 
-// One workgroup per pair: each lane sums its tokens in float64, then lanes
-// and waves join in a fixed order.
-__global__ __launch_bounds__(kThreads) void pair_kernel(const double* __restrict__ logps64, const float* __restrict__ ref,
-                                                       const int64_t* __restrict__ labels, const int64_t* __restrict__ offsets,
-                                                       int64_t tokens, int kind, float beta, float smoothing, int average,
-                                                       float* __restrict__ loss, float* __restrict__ margin,
-                                                       float* __restrict__ slope) {
-  __shared__ double sums[2][kWaves], counts[2][kWaves];
+// One workgroup per pair, half of its waves for each side: a lane sums its
+// tokens in float64, then lanes and waves join in a fixed order.
+__global__ __launch_bounds__(2 * kThreads) void pair_kernel(const double* __restrict__ logps64, const float* __restrict__ ref,
+                                                           const int64_t* __restrict__ labels,
+                                                           const int64_t* __restrict__ offsets, int64_t tokens, int kind,
+                                                           float beta, float smoothing, int average,
+                                                           float* __restrict__ loss, float* __restrict__ margin,
+                                                           float* __restrict__ slope) {
+  __shared__ double sums[2 * kWaves], counts[2 * kWaves];
   const int64_t p = blockIdx.x;
-#pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    const int64_t a = clamp_row(offsets[2 * p + side], tokens), b = clamp_row(offsets[2 * p + side + 1], tokens);
-    double s = 0.0, n = 0.0;
-    for (int64_t t = a + threadIdx.x; t < b; t += kThreads)
-      if (labels[t] >= 0) {
-        s += logps64[t] - (ref ? static_cast<double>(ref[t]) : 0.0);
-        n += 1.0;
-      }
-    s = group_sum_d<64>(s);
-    n = group_sum_d<64>(n);
-    if ((threadIdx.x & 63) == 0) {
-      sums[side][threadIdx.x >> 6] = s;
-      counts[side][threadIdx.x >> 6] = n;
+  const int side = threadIdx.x / kThreads, wave = threadIdx.x >> 6;
+  const int64_t a = clamp_row(offsets[2 * p + side], tokens), b = clamp_row(offsets[2 * p + side + 1], tokens);
+  double s = 0.0, n = 0.0;
+  for (int64_t t = a + threadIdx.x % kThreads; t < b; t += kThreads) {
+    const double lp = logps64[t], rf = ref ? static_cast<double>(ref[t]) : 0.0;
+    if (labels[t] >= 0) {
+      s += lp - rf;
+      n += 1.0;
     }
+  }
+  s = group_sum_d<64>(s);
+  n = group_sum_d<64>(n);
+  if ((threadIdx.x & 63) == 0) {
+    sums[wave] = s;
+    counts[wave] = n;
   }
   __syncthreads();
   if (threadIdx.x != 0) return;
   double mean[2], per[2];
-  for (int side = 0; side < 2; ++side) {
-    double s = 0.0, n = 0.0;
+#pragma unroll
+  for (int d = 0; d < 2; ++d) {
+    s = n = 0.0;
+#pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-      s += sums[side][w];
-      n += counts[side][w];
+      s += sums[d * kWaves + w];
+      n += counts[d * kWaves + w];
     }
-    per[side] = average && n > 1.0 ? 1.0 / n : 1.0;
-    mean[side] = s * per[side];
+    per[d] = average && n > 1.0 ? 1.0 / n : 1.0;
+    mean[d] = s * per[d];
   }
   const double h = mean[0] - mean[1], bt = beta, eps = smoothing;
   double l, d;
@@ -158,6 +185,8 @@ __device__ __forceinline__ int64_t sequence_of(const int64_t* offsets, int64_t s
   return lo;
 }
 
+// Rows from the last to the first: the loss's rows were read in the other
+// order, so its last ones are still in the last-level cache.
 template <int TY>
 __global__ __launch_bounds__(kThreads) void row_grad_kernel(const typename Elem<TY>::type* logits, int64_t vocab,
                                                            int64_t stride, const int64_t* __restrict__ labels,
@@ -165,7 +194,7 @@ __global__ __launch_bounds__(kThreads) void row_grad_kernel(const typename Elem<
                                                            const float2* __restrict__ stats, const float* __restrict__ slope,
                                                            const float* __restrict__ grad_loss,
                                                            typename Elem<TY>::type* dlogits, int64_t out_stride) {
-  const int64_t t = blockIdx.x;
+  const int64_t t = static_cast<int64_t>(gridDim.x) - 1 - blockIdx.x;
   const int64_t label = labels[t];
   const int64_t seq = label < 0 ? -1 : sequence_of(offsets, sequences, t);
   auto* out = dlogits + t * out_stride;
@@ -189,12 +218,20 @@ __global__ __launch_bounds__(kThreads) void row_grad_kernel(const typename Elem<
   }
 }
 
+// Few long rows get workgroups of 1024 lanes, so that a row is a few rounds of
+// loads; otherwise 256 lanes a row fill the CUs.
+constexpr int64_t kFewTokens = 512, kLongRow = 8192;
+
 template <int TY>
 hipError_t stats_as(const void* logits, int64_t tokens, int64_t vocab, int64_t stride, const int64_t* labels, float* logps,
                     double* logps64, float* stats, hipStream_t stream) {
-  hipLaunchKernelGGL((row_stats_kernel<TY>), dim3(static_cast<unsigned>(tokens)), dim3(kThreads), 0, stream,
-                     static_cast<const typename Elem<TY>::type*>(logits), vocab, stride, labels, logps, logps64,
-                     reinterpret_cast<float2*>(stats));
+  const auto* z = static_cast<const typename Elem<TY>::type*>(logits);
+  if (tokens <= kFewTokens && vocab >= kLongRow)
+    hipLaunchKernelGGL((row_stats_kernel<TY, 1024>), dim3(static_cast<unsigned>(tokens)), dim3(1024), 0, stream, z, vocab,
+                       stride, labels, logps, logps64, reinterpret_cast<float2*>(stats));
+  else
+    hipLaunchKernelGGL((row_stats_kernel<TY, kThreads>), dim3(static_cast<unsigned>(tokens)), dim3(kThreads), 0, stream, z,
+                       vocab, stride, labels, logps, logps64, reinterpret_cast<float2*>(stats));
   return hipGetLastError();
 }
 
@@ -218,7 +255,7 @@ hipError_t grad_as(const void* logits, int64_t tokens, int64_t vocab, int64_t st
 }
 
 // rows are workgroups: fewer than 2^32 threads a launch
-constexpr int64_t kMaxTokens = (int64_t{1} << 32) / kThreads - 1;
+constexpr int64_t kMaxTokens = (int64_t{1} << 32) / (2 * kThreads) - 1;
 
 const char* bad_logits(const void* logits, int type, int64_t tokens, int64_t vocab, int64_t stride, const int64_t* labels) {
   if (const char* why = bad_matrix(tokens, vocab, stride, type)) return why;
@@ -266,7 +303,7 @@ int casgd_pref_loss(const void* logits, int type, int64_t tokens, int64_t vocab,
   double* logps64 = static_cast<double*>(workspace);
   hipError_t e = mx::launch_stats(type, logits, tokens, vocab, stride, labels, logps, logps64, stats, stream);
   if (e == hipSuccess) {
-    hipLaunchKernelGGL(mx::pair_kernel, dim3(static_cast<unsigned>(pairs)), dim3(mx::kThreads), 0, stream, logps64, ref_logps,
+    hipLaunchKernelGGL(mx::pair_kernel, dim3(static_cast<unsigned>(pairs)), dim3(2 * mx::kThreads), 0, stream, logps64, ref_logps,
                        labels, offsets, tokens, loss_kind, beta, smoothing, average, loss, margin, slope);
     e = hipGetLastError();
   }

@@ -366,8 +366,8 @@ int casgd_mx4_linear(const void* x, int x_type, int64_t m, int64_t k, int64_t x_
  *                          checkpointed in MX8 (the rounding of Q4 taken as
  *                          the identity); accumulate != 0 adds to dw.  t = 0
  *                          gives zeros (or leaves dw).
- * n, k <= 2^22.  workspace: casgd_mx_grad_workspace bytes at least, 256-byte
- * aligned, of the same arguments (weight: 0 for the input's gradient, 1 for
+ * n, k <= 2^22.  workspace: casgd_mx_grad_workspace bytes at least (0: none),
+ * 256-byte aligned, of the same arguments (weight: 0 for the input's gradient, 1 for
  * the weights', whose t is m; dy is only looked at for its alignment): the
  * coded matrix as bf16, and a copy of dy unless it is bf16 with 16-byte
  * aligned rows. */

@@ -108,7 +108,8 @@ def test_quantise_ties_extremes_and_non_finite_blocks(fmt):
 
 LINEAR = [(1, 1, 1), (1, 32, 5), (1, 2000, 300), (2, 129, 64), (5, 640, 33), (15, 4096, 17), (16, 512, 16), (17, 96, 130),
           (31, 256, 257), (33, 1000, 128), (64, 128, 64), (65, 160, 300), (100, 2000, 259), (128, 512, 256),
-          (129, 700, 127), (257, 384, 513), (300, 64, 1024)]
+          (129, 700, 127), (257, 384, 513), (300, 64, 1024),
+          (16, 8200, 2100), (24, 2300, 300), (31, 4000, 40), (7, 2560, 12400), (32, 2176, 12289), (20, 9000, 33), (60, 3000, 200)]
 
 
 @pytest.mark.parametrize("m,k,n", LINEAR)
@@ -175,16 +176,23 @@ def test_gradients(m, n, k):
         assert torch.equal(got, B.mx8_grad_weight(strided(dy, 5, 3), x, out_dtype=T[out]))
 
 
-@pytest.mark.parametrize("m,n,k", [(70, 3900, 4200), (3900, 65, 4200), (3900, 4200, 90), (1000, 1003, 1500), (4096, 40, 3900)])
+@pytest.mark.parametrize("m,n,k", [(70, 3900, 4200), (3900, 65, 4200), (3900, 4200, 90), (1000, 1003, 1500), (4096, 40, 3900), (1700, 1801, 1900), (4100, 4100, 300)])
 def test_gradients_of_many_tiles(m, n, k):
     w, x = stored(values((n, k), 4), "mx4"), stored(values((m, k), 5), "mx8")
     wv = H.dequantize(w.codes.cpu().numpy(), w.scales.cpu().numpy(), k, "mx4")
     xv = H.dequantize(x.codes.cpu().numpy(), x.scales.cpu().numpy(), k, "mx8")
-    for dtype, out in (("bf16", "bf16"), ("fp32", "fp32")):
+    for dtype, out in (("bf16", "bf16"), ("fp32", "fp32"), ("fp16", "fp32")):
         dy = cuda(values((m, n), 6) * 0.01, dtype)
         dyv = host(dy)
-        close(B.mx4_grad_input(dy, w, T[out]), dyv, wv, out)
-        close(B.mx8_grad_weight(dy, x, out_dtype=T[out]), dyv.T, xv, out)
+        dx, dw = B.mx4_grad_input(dy, w, T[out]), B.mx8_grad_weight(dy, x, out_dtype=T[out])
+        close(dx, dyv, wv, out)
+        close(dw, dyv.T, xv, out)
+        wide = strided(torch.ones((n, k), dtype=T[out], device="cuda"), 3, 1)
+        B.mx8_grad_weight(dy, x, out=wide, accumulate=True)
+        close(wide, dyv.T, xv, out, base=1.0)
+        for view in (strided(dy, 5, 3), strided(dy, 16 - n % 8, 8)):
+            assert torch.equal(dx, B.mx4_grad_input(view, w, T[out]))
+            assert torch.equal(dw, B.mx8_grad_weight(view, x, out_dtype=T[out]))
 
 
 def test_gradient_of_no_rows():

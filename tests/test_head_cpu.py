@@ -44,9 +44,9 @@ def test_quantise_refusals(args, text):
 def test_product_refusals():
     lib = B.load()
     assert lib.casgd_mx4_linear_workspace(4, 64, 8) == 0 and lib.casgd_mx4_linear_workspace(4, 0, 8) == -1
-    need = lib.casgd_mx4_linear_workspace(40, 64, 8)
-    assert need >= 40 * (64 + 4)
-    ok = (P, B.BF16, 40, 64, 64, P, P, 8, P, B.BF16, 8, P, need, None)
+    need = lib.casgd_mx4_linear_workspace(400, 64, 8)
+    assert need >= 400 * (64 + 4)
+    ok = (P, B.BF16, 400, 64, 64, P, P, 8, P, B.BF16, 8, P, need, None)
 
     def linear(at, value, text):
         refused(lib.casgd_mx4_linear(*ok[:at], value, *ok[at + 1:]), text)
@@ -58,28 +58,31 @@ def test_product_refusals():
 
 def test_gradient_refusals():
     lib = B.load()
-    need = lib.casgd_mx_grad_workspace(0, 4, 8, 64, P, B.FP32, 8)
-    assert need >= 32 * 128 * 2 and lib.casgd_mx_grad_workspace(0, 4, 8, 64, P, B.FP8, 8) == -1
-    ok = (P, B.FP32, 4, 8, 8, P, P, 64, P, B.FP32, 64, P, need, None)
+    assert lib.casgd_mx_grad_workspace(0, 4, 8, 64, P, B.FP32, 8) == 0
+    assert lib.casgd_mx_grad_workspace(0, 4, 8, 64, P, B.FP8, 8) == -1
+    m, n, k = 4000, 1000, 1500
+    need = lib.casgd_mx_grad_workspace(0, m, n, k, P, B.FP32, n)
+    assert need >= 2 * 1024 * 1536 + 3 * 2 * m * n
+    ok = (P, B.FP32, m, n, n, P, P, k, P, B.FP32, k, P, need, None)
 
     def grad_input(at, value, text):
         refused(lib.casgd_mx4_grad_input(*ok[:at], value, *ok[at + 1:]), text)
 
     for at in (0, 5, 6, 8, 11):
         grad_input(at, None, "NULL")
-    grad_input(1, B.FP8, "element type"), grad_input(9, 9, "element type"), grad_input(4, 7, "row stride")
-    grad_input(10, 63, "row stride"), grad_input(12, need - 1, "workspace"), grad_input(11, ODD, "aligned")
+    grad_input(1, B.FP8, "element type"), grad_input(9, 9, "element type"), grad_input(4, n - 1, "row stride")
+    grad_input(10, k - 1, "row stride"), grad_input(12, need - 1, "workspace"), grad_input(11, ODD, "aligned")
     grad_input(2, 2 ** 30, "rows")
-    need = lib.casgd_mx_grad_workspace(1, 4, 8, 64, P, B.FP32, 8)
-    okw = (P, B.FP32, 4, 8, 8, P, P, 64, P, B.FP32, 64, 0, P, need, None)
+    need = lib.casgd_mx_grad_workspace(1, m, n, k, P, B.FP32, n)
+    okw = (P, B.FP32, m, n, n, P, P, k, P, B.FP32, k, 0, P, need, None)
 
     def grad_weight(at, value, text):
         refused(lib.casgd_mx8_grad_weight(*okw[:at], value, *okw[at + 1:]), text)
 
     for at in (0, 5, 6, 8, 12):
         grad_weight(at, None, "NULL")
-    grad_weight(1, B.FP8, "element type"), grad_weight(9, 9, "element type"), grad_weight(4, 7, "row stride")
-    grad_weight(10, 63, "row stride"), grad_weight(13, need - 1, "workspace"), grad_weight(12, ODD, "aligned")
+    grad_weight(1, B.FP8, "element type"), grad_weight(9, 9, "element type"), grad_weight(4, n - 1, "row stride")
+    grad_weight(10, k - 1, "row stride"), grad_weight(13, need - 1, "workspace"), grad_weight(12, ODD, "aligned")
     refused(lib.casgd_mx4_grad_input(P, B.BF16, 4, 2 ** 23, 2 ** 23, P, P, 64, P, B.BF16, 64, P, need, None), "2^22")
 
 
