@@ -127,7 +127,16 @@ __device__ __forceinline__ void store1(typename Elem<TY>::type* p, float v) {
     *p = narrow1<TY>(v);
 }
 
-template <int TY>
+// STREAM: stores that leave the caches to what is read again
+template <bool STREAM>
+__device__ __forceinline__ void store16(u32x4 v, void* p) {
+  if constexpr (STREAM)
+    __builtin_nontemporal_store(v, static_cast<u32x4_any*>(p));
+  else
+    *static_cast<u32x4_any*>(p) = v;
+}
+
+template <int TY, bool STREAM = false>
 __device__ __forceinline__ void store8(typename Elem<TY>::type* row, int64_t c, int64_t cols, const float v[8]) {
   if (c + 8 <= cols) {
     if constexpr (TY == kF32) {
@@ -137,13 +146,13 @@ __device__ __forceinline__ void store8(typename Elem<TY>::type* row, int64_t c, 
         a[i] = __float_as_uint(v[i]);
         b[i] = __float_as_uint(v[4 + i]);
       }
-      *reinterpret_cast<u32x4_any*>(row + c) = a;
-      *reinterpret_cast<u32x4_any*>(row + c + 4) = b;
+      store16<STREAM>(a, row + c);
+      store16<STREAM>(b, row + c + 4);
     } else {
       u32x4 a;
 #pragma unroll
       for (int i = 0; i < 4; ++i) a[i] = narrow2<TY>(v[2 * i], v[2 * i + 1]);
-      *reinterpret_cast<u32x4_any*>(row + c) = a;
+      store16<STREAM>(a, row + c);
     }
   } else {
 #pragma unroll

@@ -167,6 +167,26 @@ def test_all_masked_and_empty():
     assert abs(float(fwd.loss) - np.log(2)) < 1e-7 and B.pref_grad(fwd, gpu(g)).shape == (0, 40)
 
 
+def test_long_gradient():
+    # over 128 MiB: streamed stores; rows against torch's float64 on a sample
+    tokens, vocab = 1100, 65543
+    z, labels, offsets, ref, g = make(tokens, vocab, 2, "bf16", 14)
+    fwd = B.pref_loss(z, gpu(labels), gpu(offsets), gpu(ref))
+    d = B.pref_grad(fwd, gpu(g))
+    slope = host(fwd.slope)
+    for t in (0, 1, 500, 1099, int(offsets[1]), int(offsets[2])):
+        t = min(t, tokens - 1)
+        row, got = host(z[t]), host(d[t])
+        s = max(i for i in range(4) if offsets[i] <= t)
+        want = np.zeros(vocab)
+        if labels[t] >= 0:
+            q = np.exp(row - row.max())
+            want = -slope[s] * float(g[s // 2]) * q / q.sum()
+            want[labels[t]] += slope[s] * float(g[s // 2])
+        # the exponential's and the sum's errors (2 * 30 + 2 * 280) 2^-24, then half a bf16 step
+        assert (np.abs(got - want) <= (2.0 ** -8 + 700 * U) * np.abs(want) + 700 * U * np.abs(want).max()).all()
+
+
 def test_bad_offsets_stay_inside():
     # not decreasing is the caller's part; values past the ends are clamped
     z, labels, offsets, ref, g = make(6, 40, 1, "fp32", 9)
