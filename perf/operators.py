@@ -174,7 +174,8 @@ def run_own(state, case):
         x8 = B.mx_quantize(state["x"], "mx8")
         return {"dx": B.mx4_grad_input(state["dy"], w4, out), "dw": B.mx8_grad_weight(state["dy"], x8)}
     fwd = B.pref_loss(state["logits"], state["labels"], state["offsets"], state["ref"], case["beta"],
-                      loss=case["loss"], smoothing=case["smoothing"], average=case["average"])
+                      loss=case["loss"], smoothing=case["smoothing"] if case["loss"] == "logistic" else 0.0,
+                      average=case["average"])
     return {"loss": fwd.loss, "logps": fwd.logps, "dlogits": B.pref_grad(fwd, state["grad_loss"])}
 
 
