@@ -3,11 +3,10 @@
 // are.
 //
 // A wave owns a 64 x 64 tile of the output and every D-th slice of 32 of the
-// summed index; it widens its slice of the codes (and of dy, where dy's rows
-// are the summed index) to bf16 in LDS of its own and reads fragments from
-// there, so the loop has no barrier.  The D waves of a tile then add their
-// sums in a fixed order.  Bound by latency: the next slice's loads are in
-// flight while one is computed.
+// summed index; it widens its slice of the codes and of dy to bf16 in LDS of
+// its own and reads fragments from there, so the loop has no barrier.  The D
+// waves of a tile then add their sums in a fixed order.  Bound by latency: the
+// next slices' loads are in flight while one is computed.
 #pragma once
 
 #include <type_traits>
@@ -58,26 +57,46 @@ __device__ __forceinline__ void split8(float v[8], u32x4 (&out)[PARTS]) {
 template <int TY>
 constexpr int kParts = TY == kBF16 ? 1 : TY == kF16 ? 2 : 3;
 
-// 32 codes of one block to bf16
-__device__ __forceinline__ void widen_block4(u32x4 w, float scale, u32x4 out[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    out[i].x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i], scale, 0));
-    out[i].y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i], scale, 1));
-    out[i].z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i], scale, 2));
-    out[i].w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i], scale, 3));
-  }
+// 8 codes of one block to bf16
+__device__ __forceinline__ u32x4 widen8_mx4(uint32_t w, float scale) {
+  u32x4 out;
+  out.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0));
+  out.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1));
+  out.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2));
+  out.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3));
+  return out;
 }
-__device__ __forceinline__ void widen_block8(u32x4 a, u32x4 b, float scale, u32x4 out[4]) {
+__device__ __forceinline__ u32x4 widen8_mx8(uint32_t lo, uint32_t hi, float scale) {
+  u32x4 out;
+  out.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false));
+  out.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true));
+  out.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false));
+  out.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true));
+  return out;
+}
+
+// 8 elements moved down by d (0 ... 8), zeros behind: what a piece that was
+// read d elements early, to stay inside its row, stands for.
+template <int TY, int WORDS>
+__device__ __forceinline__ void shift_down(u32x4 (&w)[WORDS], int d) {
+  uint32_t v[8] = {};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const u32x4 w = i < 2 ? a : b;
-    const int k = (i & 1) * 2;
-    out[i].x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[k], scale, false));
-    out[i].y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[k], scale, true));
-    out[i].z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[k + 1], scale, false));
-    out[i].w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[k + 1], scale, true));
+  for (int i = 0; i < 4 * WORDS; ++i) v[i] = d & 8 ? 0u : w[i / 4][i & 3];
+  if constexpr (TY == kF32) {
+#pragma unroll
+    for (int by = 4; by > 0; by /= 2)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = d & by ? (i + by < 8 ? v[i + by] : 0u) : v[i];
+  } else {
+#pragma unroll
+    for (int by = 2; by > 0; by /= 2)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = d & (2 * by) ? (i + by < 4 ? v[i + by] : 0u) : v[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = d & 1 ? (v[i] >> 16) | (i < 3 ? v[i + 1] << 16 : 0u) : v[i];
   }
+#pragma unroll
+  for (int i = 0; i < 4 * WORDS; ++i) w[i / 4][i & 3] = v[i];
 }
 
 struct SmallArgs {
@@ -91,9 +110,9 @@ struct SmallArgs {
   int region;                // LDS bytes of a wave
 };
 
-template <int TY, bool ACROSS>
+template <int TY>
 constexpr int small_region(int ways) {
-  const int stage = 4096 * (1 + (ACROSS ? kParts<TY> : 0));
+  const int stage = 4096 * (1 + kParts<TY>);
   return ways > 1 && stage < 16384 ? 16384 : stage;  // a wave's 64 x 64 sums
 }
 
@@ -114,45 +133,40 @@ __global__ __launch_bounds__(512) void mx_small_grad_kernel(SmallArgs g, const t
   uint8_t* mine = smem + wave * g.region;
   const int half = lane >> 5, r32 = lane & 31;
 
-  // staging: two lanes a row of the slice, 32 elements (one block) each
-  const int srow = lane >> 1, shalf = lane & 1;
+  // Staging reads whole rows: a load is 16 rows of MX8 (4 lanes of 16 codes
+  // each) or 32 of MX4 (2 lanes of 32), and 8 rows of dy (8 lanes of 8
+  // elements; 16 rows of 4 lanes where its rows are the output); lanes that each took a row's run of their own touched 64 lines
+  // a load and were bound by the address units.
   constexpr int NW = FMT == kMx8 ? 2 : 1;
   constexpr int XW = TY == kF32 ? 2 : 1;
-  auto fetch = [&](int s, u32x4 (&c)[NW], float& scale, u32x4 (&xw)[4][XW]) {
-    const int64_t t = static_cast<int64_t>(s) * 32 + srow;
-    const bool in = t < g.depth;
-    const u32x4 zero = {0u, 0u, 0u, 0u};
-    const int64_t at = t * g.ld + j0 + shalf * 32;  // in elements
-    if constexpr (FMT == kMx8) {
-      c[0] = in ? *reinterpret_cast<const u32x4*>(g.codes + at) : zero;
-      c[1] = in ? *reinterpret_cast<const u32x4*>(g.codes + at + 16) : zero;
-    } else {
-      c[0] = in ? *reinterpret_cast<const u32x4*>(g.codes + at / 2) : zero;
+  const int crow = FMT == kMx8 ? lane >> 2 : lane >> 1, cpart = FMT == kMx8 ? lane & 3 : lane & 1;
+  const int xrow = ACROSS ? lane >> 3 : lane >> 2, xpiece = ACROSS ? lane & 7 : lane & 3;
+  // A slice's loads, all of them unconditional: behind a branch that may skip
+  // some, the compiler could no longer count them and would wait for every
+  // load of the next slice too.  Rows past the end read the last one, pieces
+  // that would pass their row's end start early; compute() puts both right.
+  const int64_t xlast = g.x_cols - 8;  // at least 0
+  auto xcol = [&](int s) { return (ACROSS ? i0 : static_cast<int64_t>(s) * 32) + xpiece * 8; };
+  auto fetch = [&](int s_, u32x4 (&c)[NW], float (&scale)[NW], u32x4 (&xw)[4][XW]) {
+    const int s = s_ < g.slices ? s_ : g.slices - 1;
+#pragma unroll
+    for (int h = 0; h < NW; ++h) {
+      int64_t t = static_cast<int64_t>(s) * 32 + h * 16 + crow;
+      if (t >= g.depth) t = g.depth - 1;
+      const int64_t at = t * g.ld + j0 + cpart * (FMT == kMx8 ? 16 : 32);  // in elements
+      c[h] = *reinterpret_cast<const u32x4*>(g.codes + (FMT == kMx8 ? at : at / 2));
+      scale[h] = scale_value(g.scales[at >> 5]);
     }
-    scale = in ? scale_value(g.scales[at >> 5]) : 1.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      // across: 8 columns of row t; along: fragment i (row tile i / 2, half-slice i % 2)
-      const int64_t row = ACROSS ? t : i0 + (i >> 1) * 32 + r32;
-      const int64_t col = ACROSS ? i0 + shalf * 32 + i * 8 : static_cast<int64_t>(s) * 32 + (i & 1) * 16 + half * 8;
-      const bool ok = row < (ACROSS ? g.depth : g.rows);
+      int64_t row = ACROSS ? static_cast<int64_t>(s) * 32 + i * 8 + xrow : i0 + i * 16 + xrow;
+      const int64_t rows = ACROSS ? g.depth : g.rows;
+      if (row >= rows) row = rows - 1;
+      int64_t col = xcol(s);
+      if (col > xlast) col = xlast;
       const auto* p = x + row * g.x_stride + col;
 #pragma unroll
-      for (int h = 0; h < XW; ++h) xw[i][h] = zero;
-      if (ok && col + 8 <= g.x_cols) {
-#pragma unroll
-        for (int h = 0; h < XW; ++h) xw[i][h] = *reinterpret_cast<const u32x4_any*>(p + 4 * h);
-      } else if (ok) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t bits = col + e < g.x_cols ? __builtin_bit_cast(
-              typename std::conditional<TY == kF32, uint32_t, uint16_t>::type, p[e]) : 0u;
-          if constexpr (TY == kF32)
-            xw[i][e / 4][e & 3] = bits;
-          else
-            xw[i][0][e / 2] |= bits << (16 * (e & 1));
-        }
-      }
+      for (int h = 0; h < XW; ++h) xw[i][h] = *reinterpret_cast<const u32x4_any*>(p + 4 * h);
     }
   };
   auto parts_of_raw = [&](const u32x4 (&r)[XW], u32x4 (&w)[PARTS]) {
@@ -170,7 +184,9 @@ __global__ __launch_bounds__(512) void mx_small_grad_kernel(SmallArgs g, const t
 
   // 16-byte piece p of staged row t lies at piece p XOR 4 (t / 2 mod 2): the 32
   // lanes of a transposed read's cycle take 64 bytes of four rows of 128 bytes
-  const int sx = ((srow >> 1) & 1) << 2;
+  auto staged = [&](int t, int piece) { return t * 128 + ((piece ^ (((t >> 1) & 1) << 2)) * 16); };
+  // rows of the output: 64 bytes each, pieces at piece XOR (row / 4 mod 4)
+  auto staged_along = [&](int r, int piece) { return r * 64 + ((piece ^ ((r >> 2) & 3)) * 16); };
   const int trow = 8 * half + ((lane & 15) >> 2);
   const int tlow = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1), tx = ((lane & 15) >> 3) << 2;
   const int tbyte = (lane & 1) * 8;
@@ -191,32 +207,44 @@ __global__ __launch_bounds__(512) void mx_small_grad_kernel(SmallArgs g, const t
       for (int e = 0; e < 16; ++e) acc[a][b][e] = 0.f;
 
   if (live && part < g.slices) {
-    auto compute = [&](const u32x4 (&cc)[NW], float cscale, const u32x4 (&cx)[4][XW]) {
-      u32x4 w[4];
-      if constexpr (FMT == kMx8)
-        widen_block8(cc[0], cc[1], cscale, w);
-      else
-        widen_block4(cc[0], cscale, w);
+    const bool xedge = ACROSS && i0 + 64 > g.x_cols;
+    auto compute = [&](int s, u32x4 (&cc)[NW], float (&scale)[NW], u32x4 (&cx)[4][XW]) {
+      if (xedge || s == g.slices - 1) {
+        const u32x4 zero = {0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4*>(mine + srow * 128 + (((shalf * 4 + i) ^ sx) * 16)) = w[i];
-      bf16x8 fx[2][2][PARTS];  // [row tile][half-slice][part]
-      if constexpr (ACROSS) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          u32x4 q[PARTS];
-          parts_of_raw(cx[i], q);
-#pragma unroll
-          for (int p = 0; p < PARTS; ++p)
-            *reinterpret_cast<u32x4*>(mine + 4096 * (1 + p) + srow * 128 + (((shalf * 4 + i) ^ sx) * 16)) = q[p];
-        }
-      } else {
+        for (int h = 0; h < NW; ++h)
+          if (static_cast<int64_t>(s) * 32 + h * 16 + crow >= g.depth) {
+            cc[h] = zero;
+            scale[h] = 1.f;
+          }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          u32x4 q[PARTS];
-          parts_of_raw(cx[i], q);
-#pragma unroll
-          for (int p = 0; p < PARTS; ++p) fx[i >> 1][i & 1][p] = __builtin_bit_cast(bf16x8, q[p]);
+          const int64_t early = xcol(s) - xlast;
+          int d = early < 0 ? 0 : early < 8 ? static_cast<int>(early) : 8;
+          if (ACROSS && static_cast<int64_t>(s) * 32 + i * 8 + xrow >= g.depth) d = 8;
+          shift_down<TY, XW>(cx[i], d);
         }
+      }
+#pragma unroll
+      for (int h = 0; h < NW; ++h) {
+        const int t = h * 16 + crow;
+        if constexpr (FMT == kMx8) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<u32x4*>(mine + staged(t, cpart * 2 + i)) = widen8_mx8(cc[h][2 * i], cc[h][2 * i + 1], scale[h]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<u32x4*>(mine + staged(t, cpart * 4 + i)) = widen8_mx4(cc[h][i], scale[h]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        u32x4 q[PARTS];
+        parts_of_raw(cx[i], q);
+        const int at = ACROSS ? staged(i * 8 + xrow, xpiece) : staged_along(i * 16 + xrow, xpiece);
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) *reinterpret_cast<u32x4*>(mine + 4096 * (1 + p) + at) = q[p];
       }
       // the wave's own LDS: its accesses are carried out in order
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -234,7 +262,7 @@ __global__ __launch_bounds__(512) void mx_small_grad_kernel(SmallArgs g, const t
             if constexpr (ACROSS)
               f = read_across(mine + 4096 * (1 + p), b, k);
             else
-              f = fx[b][k][p];
+              f = *reinterpret_cast<const bf16x8*>(mine + 4096 * (1 + p) + staged_along(b * 32 + r32, 2 * k + half));
 #pragma unroll
             for (int a = 0; a < 2; ++a) acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fc[a], f, acc[a][b], 0, 0, 0);
           }
@@ -242,17 +270,18 @@ __global__ __launch_bounds__(512) void mx_small_grad_kernel(SmallArgs g, const t
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
     };
-    // two slices in flight; one past the end is zeros, its rows being past the
-    // summed index
-    u32x4 c0[NW], c1[NW], x0[4][XW], x1[4][XW];
-    float s0, s1;
-    fetch(part, c0, s0, x0);
-    fetch(part + g.ways, c1, s1, x1);
-    for (int s = part; s < g.slices; s += 2 * g.ways) {
-      compute(c0, s0, x0);
-      fetch(s + 2 * g.ways, c0, s0, x0);
-      compute(c1, s1, x1);
-      fetch(s + 3 * g.ways, c1, s1, x1);
+    constexpr int FLIGHT = 2;  // slices in flight; four were no faster
+    u32x4 c[FLIGHT][NW], xw[FLIGHT][4][XW];
+    float scale[FLIGHT][NW];
+#pragma unroll
+    for (int f = 0; f < FLIGHT; ++f) fetch(part + f * g.ways, c[f], scale[f], xw[f]);
+    for (int s = part; s < g.slices; s += FLIGHT * g.ways) {
+#pragma unroll
+      for (int f = 0; f < FLIGHT; ++f) {
+        const int at = s + f * g.ways;
+        if (at < g.slices) compute(at, c[f], scale[f], xw[f]);
+        fetch(at + FLIGHT * g.ways, c[f], scale[f], xw[f]);
+      }
     }
   }
 

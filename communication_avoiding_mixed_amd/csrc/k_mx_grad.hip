@@ -121,18 +121,23 @@ Plan plan_of(bool across, int64_t m, int64_t n, int64_t k, int type, const void*
   // The one-launch form: as many waves share a tile's summed index as fill the
   // CUs with 8 waves each, while every wave has a slice.  Against the tiled
   // form (widening, copying and adding up in launches of their own), rows x n
-  // x k, bf16 / float32 dy, us a call, dx and dW:
-  //   37 x 1000 x 2000    11 / 16 and 11 / 13   (tiled 16 / 21 and 13 / 17)
-  //   1024 x 1024 x 1024  12 / 20 and 11 / 21   (tiled 22 / 31 and 22 / 32)
-  //   2048 x 2048 x 1024  29 / 57 and 28 / 55   (tiled 31 / 68 and 33 / 68)
-  //   64 x 4096 x 4096    33 / 54               (tiled 30 / 47: 16 slices a wave on 64 CUs)
-  //   4096 x 512 x 512    dW 28 / 55            (tiled 21 / 33: 16 slices a wave on 64 CUs)
-  // so it is taken up to this work while a wave has few slices or the CUs are full.
+  // x k, us a call with bf16 / float32 dy, dx and dW:
+  //   37 x 1000 x 2000     9 / 13 and 9 / 11     (tiled 16 / 21 and 13 / 16)
+  //   1024 x 1024 x 1024   9 / 15 and 9 / 16     (tiled 22 / 30 and 23 / 31)
+  //   2048 x 2048 x 1024  25 / 43 and 24 / 47    (tiled 30 / 64 and 32 / 66)
+  //   4096 x 4096 x 1024  72 / 158 and 67 / 152  (tiled 64 / 192 and 66 / 197)
+  // Where tiles are few and the summed index long, a wave has many slices and
+  // most CUs none:
+  //   360 x 6362 x 660    dx 35 / 57             (tiled 29 / 43; 25 slices)
+  //   4096 x 512 x 512    dW 20 / 39             (tiled 21 / 32; 16 slices)
+  // float32 parts cost the tiled form more (three passes over the codes), and
+  // cost this one more where dy has to be transposed (dW).
   p.tiles64 = ((p.rows + 63) / 64) * ((p.cols + 63) / 64);
   p.ways = 1;
-  while (p.ways < 8 && p.tiles64 * p.ways < 2048 && p.stages > p.ways) p.ways *= 2;
-  p.small = static_cast<double>(p.depth) * p.rows * p.cols <= 4.5e9 &&
-            (p.stages <= 8 * p.ways || p.tiles64 * p.ways >= 2048);
+  while (p.ways < 8 && p.tiles64 * p.ways * 2 <= 2048 && p.stages > p.ways) p.ways *= 2;
+  const double most = p.parts == 1 ? 6e9 : p.parts == 2 ? 18e9 : 24e9;
+  p.small = n >= 8 && static_cast<double>(p.depth) * p.rows * p.cols <= most &&
+            (p.tiles64 * p.ways >= 1024 || p.stages <= p.ways * (across ? 16 / p.parts : 16));
   if (p.small) {
     p.c_bytes = p.x_bytes = p.s_bytes = 0;
     return p;
@@ -208,7 +213,7 @@ template <int TY, bool ACROSS, int OUT>
 hipError_t small_as(const Plan& p, const void* dy, int64_t dy_stride, const uint8_t* codes, const uint8_t* scales, void* out,
                     int64_t stride, int accumulate, hipStream_t stream) {
   auto* kernel = mx_small_grad_kernel<TY, ACROSS, OUT>;
-  constexpr int most = 8 * small_region<TY, ACROSS>(8);
+  constexpr int most = 8 * small_region<TY>(8);
   static const hipError_t allowed =
       hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, most);
   if (allowed != hipSuccess) return allowed;
@@ -225,7 +230,7 @@ hipError_t small_as(const Plan& p, const void* dy, int64_t dy_stride, const uint
   g.tiles = static_cast<uint32_t>(p.tiles64);
   g.slices = p.stages;
   g.ways = p.ways;
-  g.region = small_region<TY, ACROSS>(g.ways);
+  g.region = small_region<TY>(g.ways);
   const uint32_t per = 8 / g.ways;
   hipLaunchKernelGGL(kernel, dim3((g.tiles + per - 1) / per), dim3(512), 8 * g.region, stream, g,
                      static_cast<const typename Elem<TY>::type*>(dy), static_cast<typename Elem<OUT>::type*>(out), stride,

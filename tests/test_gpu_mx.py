@@ -153,7 +153,7 @@ def test_linear_scales_over_the_whole_range():
     np.testing.assert_array_equal(y, [[2.0 ** 125, np.inf, 0], [2.0 ** -75, 2.0 ** -70, 0]])
 
 
-GRAD = [(1, 1, 1), (1, 64, 70), (2, 130, 33), (31, 32, 64), (32, 300, 65), (33, 129, 200), (37, 1000, 500), (64, 64, 64),
+GRAD = [(1, 1, 1), (40, 5, 70), (33, 8, 40), (3, 9, 40), (70, 71, 33), (40, 66, 33), (65, 15, 96), (1, 64, 70), (2, 130, 33), (31, 32, 64), (32, 300, 65), (33, 129, 200), (37, 1000, 500), (64, 64, 64),
         (100, 257, 640), (128, 128, 256), (200, 520, 130), (513, 96, 100), (1500, 40, 33)]
 
 
@@ -176,7 +176,7 @@ def test_gradients(m, n, k):
         assert torch.equal(got, B.mx8_grad_weight(strided(dy, 5, 3), x, out_dtype=T[out]))
 
 
-@pytest.mark.parametrize("m,n,k", [(70, 3900, 4200), (3900, 65, 4200), (3900, 4200, 90), (1000, 1003, 1500), (4096, 40, 3900), (1700, 1801, 1900), (4100, 4100, 300)])
+@pytest.mark.parametrize("m,n,k", [(70, 3900, 4200), (3900, 65, 4200), (3900, 4200, 90), (1000, 1003, 1500), (4096, 40, 3900), (1700, 1801, 1900), (4100, 4100, 300), (300, 6000, 100), (6000, 100, 300)])
 def test_gradients_of_many_tiles(m, n, k):
     w, x = stored(values((n, k), 4), "mx4"), stored(values((m, k), 5), "mx8")
     wv = H.dequantize(w.codes.cpu().numpy(), w.scales.cpu().numpy(), k, "mx4")
