@@ -33,30 +33,42 @@ __device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b) {
   return {m, a.s * exp_hw(a.m - m) + b.s * exp_hw(b.m - m)};
 }
 
-// 8 logits from column c; -inf past the row's end
-template <int TY>
-__device__ __forceinline__ void load_logits(const typename Elem<TY>::type* row, int64_t c, int64_t vocab, float v[8]) {
-  if (c + 8 <= vocab) {
-    widen8<TY>(load_raw8<TY>(row + c), v);
-  } else {
+// UNROLL pieces of 8 logits from column c on, `step` columns apart, all loads
+// before the first use; -inf past the row's end
+template <int TY, int UNROLL>
+__device__ __forceinline__ void load_logits(const typename Elem<TY>::type* row, int64_t c, int step, int64_t vocab,
+                                            float (&v)[UNROLL][8]) {
+  Raw8<TY> raw[UNROLL];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < vocab ? load1<TY>(row + c + i) : -INFINITY;
+  for (int u = 0; u < UNROLL; ++u)
+    if (c + u * step + 8 <= vocab) raw[u] = load_raw8<TY>(row + c + u * step);
+#pragma unroll
+  for (int u = 0; u < UNROLL; ++u) {
+    const int64_t cu = c + u * step;
+    if (cu + 8 <= vocab) {
+      widen8<TY>(raw[u], v[u]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[u][i] = cu + i < vocab ? load1<TY>(row + cu + i) : -INFINITY;
+    }
   }
 }
 
-// One workgroup per row, four 16-byte loads of a lane in flight.  NaN: the
-// max drops NaN operands, but exp(NaN - m) in the sum keeps it.
-template <int TY, int THREADS>
-__global__ __launch_bounds__(THREADS) void row_stats_kernel(const typename Elem<TY>::type* __restrict__ logits, int64_t vocab,
-                                                           int64_t stride, const int64_t* __restrict__ labels,
-                                                           float* __restrict__ logps, double* __restrict__ logps64,
-                                                           float2* __restrict__ stats) {
-  constexpr int WAVES = THREADS / 64;
+// LANES lanes per row (64: a wave each of the workgroup's 256 lanes; 256 or
+// 1024: the workgroup), four 16-byte loads of a lane in flight.  NaN: the max
+// drops NaN operands, but exp(NaN - m) in the sum keeps it.
+template <int TY, int LANES>
+__global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void row_stats_kernel(
+    const typename Elem<TY>::type* __restrict__ logits, int64_t tokens, int64_t vocab, int64_t stride,
+    const int64_t* __restrict__ labels, float* __restrict__ logps, double* __restrict__ logps64, float2* __restrict__ stats) {
+  constexpr int WAVES = LANES / 64;
   __shared__ MaxSum part[WAVES];
-  const int64_t t = blockIdx.x;
+  const int64_t t = LANES == 64 ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  if (t >= tokens) return;
+  const int lane = threadIdx.x % LANES;
   const int64_t label = labels[t];
   if (label < 0) {
-    if (threadIdx.x == 0) {
+    if (lane == 0) {
       logps[t] = 0.f;
       if (logps64) logps64[t] = 0.0;
       if (stats) stats[t] = make_float2(0.f, 1.f);
@@ -68,18 +80,9 @@ __global__ __launch_bounds__(THREADS) void row_stats_kernel(const typename Elem<
   const float z = label < vocab ? load1<TY>(row + label) : NAN;
   MaxSum acc = {-INFINITY, 0.f};
   constexpr int UNROLL = 4;
-  for (int64_t c = static_cast<int64_t>(threadIdx.x) * 8; c < vocab; c += UNROLL * THREADS * 8) {
+  for (int64_t c = static_cast<int64_t>(lane) * 8; c < vocab; c += UNROLL * LANES * 8) {
     float v[UNROLL][8];
-    if (c + (UNROLL - 1) * THREADS * 8 + 8 <= vocab) {
-      Raw8<TY> raw[UNROLL];
-#pragma unroll
-      for (int u = 0; u < UNROLL; ++u) raw[u] = load_raw8<TY>(row + c + u * THREADS * 8);
-#pragma unroll
-      for (int u = 0; u < UNROLL; ++u) widen8<TY>(raw[u], v[u]);
-    } else {
-#pragma unroll
-      for (int u = 0; u < UNROLL; ++u) load_logits<TY>(row, c + u * THREADS * 8, vocab, v[u]);
-    }
+    load_logits<TY>(row, c, LANES * 8, vocab, v);
     float m = acc.m;
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u)
@@ -98,11 +101,14 @@ __global__ __launch_bounds__(THREADS) void row_stats_kernel(const typename Elem<
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) acc = join(acc, MaxSum{__shfl_xor(acc.m, o, 64), __shfl_xor(acc.s, o, 64)});
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = acc;
-  __syncthreads();
-  if (threadIdx.x != 0) return;
-  acc = part[0];
-  for (int w = 1; w < WAVES; ++w) acc = join(acc, part[w]);
+  if constexpr (WAVES > 1) {
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = acc;
+    __syncthreads();
+    acc = part[0];
+    if (lane == 0)
+      for (int w = 1; w < WAVES; ++w) acc = join(acc, part[w]);
+  }
+  if (lane != 0) return;
   const double lp = (static_cast<double>(z) - acc.m) - log(static_cast<double>(acc.s));
   logps[t] = static_cast<float>(lp);
   if (logps64) logps64[t] = lp;
@@ -124,12 +130,25 @@ __global__ __launch_bounds__(2 * kThreads) void pair_kernel(const double* __rest
   const int side = threadIdx.x / kThreads, wave = threadIdx.x >> 6;
   const int64_t a = clamp_row(offsets[2 * p + side], tokens), b = clamp_row(offsets[2 * p + side + 1], tokens);
   double s = 0.0, n = 0.0;
-  for (int64_t t = a + threadIdx.x % kThreads; t < b; t += kThreads) {
-    const double lp = logps64[t], rf = ref ? static_cast<double>(ref[t]) : 0.0;
-    if (labels[t] >= 0) {
-      s += lp - rf;
-      n += 1.0;
+  constexpr int UNROLL = 4;  // a long sequence's loads, four rounds in flight
+  for (int64_t t0 = a + threadIdx.x % kThreads; t0 < b; t0 += UNROLL * kThreads) {
+    double lp[UNROLL];
+    float rf[UNROLL];
+    int64_t label[UNROLL];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      const int64_t t = t0 + u * kThreads;
+      const bool in = t < b;
+      label[u] = in ? labels[t] : -1;
+      lp[u] = in ? logps64[t] : 0.0;
+      rf[u] = in && ref ? ref[t] : 0.f;
     }
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u)
+      if (label[u] >= 0) {
+        s += lp[u] - static_cast<double>(rf[u]);
+        n += 1.0;
+      }
   }
   s = group_sum_d<64>(s);
   n = group_sum_d<64>(n);
@@ -188,20 +207,23 @@ __device__ __forceinline__ int64_t sequence_of(const int64_t* offsets, int64_t s
 // Rows from the last to the first: the loss read them in the other order, so
 // its last ones are still in the last-level cache (8192 x 65536 bf16: 336 us,
 // from the first 366 us).  STREAM keeps the gradient out of that cache.
-template <int TY, bool STREAM>
-__global__ __launch_bounds__(kThreads) void row_grad_kernel(const typename Elem<TY>::type* logits, int64_t vocab,
-                                                           int64_t stride, const int64_t* __restrict__ labels,
+template <int TY, bool STREAM, int LANES>
+__global__ __launch_bounds__(kThreads) void row_grad_kernel(const typename Elem<TY>::type* logits, int64_t tokens,
+                                                           int64_t vocab, int64_t stride, const int64_t* __restrict__ labels,
                                                            const int64_t* __restrict__ offsets, int64_t sequences,
                                                            const float2* __restrict__ stats, const float* __restrict__ slope,
                                                            const float* __restrict__ grad_loss,
                                                            typename Elem<TY>::type* dlogits, int64_t out_stride) {
-  const int64_t t = static_cast<int64_t>(gridDim.x) - 1 - blockIdx.x;
+  const int64_t back = LANES == 64 ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  if (back >= tokens) return;
+  const int64_t t = tokens - 1 - back;
+  const int lane = threadIdx.x % LANES;
   const int64_t label = labels[t];
   const int64_t seq = label < 0 ? -1 : sequence_of(offsets, sequences, t);
   auto* out = dlogits + t * out_stride;
   if (seq < 0) {
     const float zero[8] = {};
-    for (int64_t c = static_cast<int64_t>(threadIdx.x) * 8; c < vocab; c += kThreads * 8) store8<TY, STREAM>(out, c, vocab, zero);
+    for (int64_t c = static_cast<int64_t>(lane) * 8; c < vocab; c += LANES * 8) store8<TY, STREAM>(out, c, vocab, zero);
     return;
   }
   const auto* row = logits + t * stride;
@@ -211,43 +233,39 @@ __global__ __launch_bounds__(kThreads) void row_grad_kernel(const typename Elem<
   const float base = st.x == -INFINITY ? 0.f : st.x;
   const float k = -coef * st.y;
   constexpr int UNROLL = 4;
-  for (int64_t c = static_cast<int64_t>(threadIdx.x) * 8; c < vocab; c += UNROLL * kThreads * 8) {
+  for (int64_t c = static_cast<int64_t>(lane) * 8; c < vocab; c += UNROLL * LANES * 8) {
     float v[UNROLL][8];
-    if (c + (UNROLL - 1) * kThreads * 8 + 8 <= vocab) {
-      Raw8<TY> raw[UNROLL];
-#pragma unroll
-      for (int u = 0; u < UNROLL; ++u) raw[u] = load_raw8<TY>(row + c + u * kThreads * 8);
-#pragma unroll
-      for (int u = 0; u < UNROLL; ++u) widen8<TY>(raw[u], v[u]);
-    } else {
-#pragma unroll
-      for (int u = 0; u < UNROLL; ++u) load_logits<TY>(row, c + u * kThreads * 8, vocab, v[u]);
-    }
+    load_logits<TY>(row, c, LANES * 8, vocab, v);
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
-      const int64_t cu = c + u * kThreads * 8;
-      if (cu >= vocab) break;
+      const int64_t cu = c + u * LANES * 8;
+      if (cu < vocab) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[u][i] = exp_hw(v[u][i] - base) * k + (cu + i == label ? coef : 0.f);
-      store8<TY, STREAM>(out, cu, vocab, v[u]);
+        for (int i = 0; i < 8; ++i) v[u][i] = exp_hw(v[u][i] - base) * k + (cu + i == label ? coef : 0.f);
+        store8<TY, STREAM>(out, cu, vocab, v[u]);
+      }
     }
   }
 }
 
 // Few long rows get workgroups of 1024 lanes, so that a row is a few rounds of
-// loads; otherwise 256 lanes a row fill the CUs.
-constexpr int64_t kFewTokens = 512, kLongRow = 8192;
+// loads; rows that a wave reads in two rounds get a wave; 256 lanes otherwise.
+constexpr int64_t kFewTokens = 512, kLongRow = 8192, kWaveRow = 4096;
 
 template <int TY>
 hipError_t stats_as(const void* logits, int64_t tokens, int64_t vocab, int64_t stride, const int64_t* labels, float* logps,
                     double* logps64, float* stats, hipStream_t stream) {
   const auto* z = static_cast<const typename Elem<TY>::type*>(logits);
+  auto* st = reinterpret_cast<float2*>(stats);
   if (tokens <= kFewTokens && vocab >= kLongRow)
-    hipLaunchKernelGGL((row_stats_kernel<TY, 1024>), dim3(static_cast<unsigned>(tokens)), dim3(1024), 0, stream, z, vocab,
-                       stride, labels, logps, logps64, reinterpret_cast<float2*>(stats));
+    hipLaunchKernelGGL((row_stats_kernel<TY, 1024>), dim3(static_cast<unsigned>(tokens)), dim3(1024), 0, stream, z, tokens,
+                       vocab, stride, labels, logps, logps64, st);
+  else if (vocab <= kWaveRow)
+    hipLaunchKernelGGL((row_stats_kernel<TY, 64>), dim3(static_cast<unsigned>((tokens + 3) / 4)), dim3(kThreads), 0, stream, z,
+                       tokens, vocab, stride, labels, logps, logps64, st);
   else
     hipLaunchKernelGGL((row_stats_kernel<TY, kThreads>), dim3(static_cast<unsigned>(tokens)), dim3(kThreads), 0, stream, z,
-                       vocab, stride, labels, logps, logps64, reinterpret_cast<float2*>(stats));
+                       tokens, vocab, stride, labels, logps, logps64, st);
   return hipGetLastError();
 }
 
@@ -266,16 +284,20 @@ hipError_t grad_as(const void* logits, int64_t tokens, int64_t vocab, int64_t st
   const auto* z = static_cast<const typename Elem<TY>::type*>(logits);
   auto* out = static_cast<typename Elem<TY>::type*>(dlogits);
   const auto* st = reinterpret_cast<const float2*>(stats);
-  const dim3 grid(static_cast<unsigned>(tokens)), block(kThreads);
+  const dim3 block(kThreads);
   // Half of the 256 MB last-level cache: a gradient that is larger would push
   // out the logits that are still to be read (the loss's next pass over
   // 8192 x 65536 bf16 135 us instead of 167); a smaller one stays for its reader.
-  if (tokens * vocab * static_cast<int64_t>(sizeof(*z)) >= (int64_t{1} << 27))
-    hipLaunchKernelGGL((row_grad_kernel<TY, true>), grid, block, 0, stream, z, vocab, stride, labels, offsets, 2 * pairs, st,
-                       slope, grad_loss, out, out_stride);
+  const bool large = tokens * vocab * static_cast<int64_t>(sizeof(*z)) >= (int64_t{1} << 27);
+  if (vocab <= kWaveRow && !large)
+    hipLaunchKernelGGL((row_grad_kernel<TY, false, 64>), dim3(static_cast<unsigned>((tokens + 3) / 4)), block, 0, stream, z,
+                       tokens, vocab, stride, labels, offsets, 2 * pairs, st, slope, grad_loss, out, out_stride);
+  else if (large)
+    hipLaunchKernelGGL((row_grad_kernel<TY, true, kThreads>), dim3(static_cast<unsigned>(tokens)), block, 0, stream, z, tokens,
+                       vocab, stride, labels, offsets, 2 * pairs, st, slope, grad_loss, out, out_stride);
   else
-    hipLaunchKernelGGL((row_grad_kernel<TY, false>), grid, block, 0, stream, z, vocab, stride, labels, offsets, 2 * pairs, st,
-                       slope, grad_loss, out, out_stride);
+    hipLaunchKernelGGL((row_grad_kernel<TY, false, kThreads>), dim3(static_cast<unsigned>(tokens)), block, 0, stream, z, tokens,
+                       vocab, stride, labels, offsets, 2 * pairs, st, slope, grad_loss, out, out_stride);
   return hipGetLastError();
 }
 
