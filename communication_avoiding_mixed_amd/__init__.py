@@ -7,4 +7,4 @@ Importing the package loads nothing native: the library is opened on first
 use of the binding and raises if it has not been built.
 """
 
-__all__ = ["binding", "synth"]
+__all__ = ["binding", "head", "synth"]

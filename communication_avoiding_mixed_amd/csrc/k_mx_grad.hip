@@ -121,21 +121,22 @@ Plan plan_of(bool across, int64_t m, int64_t n, int64_t k, int type, const void*
   // The one-launch form: as many waves share a tile's summed index as fill the
   // CUs with 8 waves each, while every wave has a slice.  Against the tiled
   // form (widening, copying and adding up in launches of their own), rows x n
-  // x k, us a call with bf16 / float32 dy, dx and dW:
-  //   37 x 1000 x 2000     9 / 13 and 9 / 11     (tiled 16 / 21 and 13 / 16)
-  //   1024 x 1024 x 1024   9 / 15 and 9 / 16     (tiled 22 / 30 and 23 / 31)
-  //   2048 x 2048 x 1024  25 / 43 and 24 / 47    (tiled 30 / 64 and 32 / 66)
-  //   4096 x 4096 x 1024  72 / 158 and 67 / 152  (tiled 64 / 192 and 66 / 197)
+  // x k, us a call with bf16 / fp16 dy, dx and dW:
+  //   37 x 1000 x 2000     9 / 11 and 9 / 9      (tiled 18 / 21 and 13 / 17)
+  //   1024 x 1024 x 1024  10 / 12 and 10 / 13    (tiled 22 / 27 and 23 / 28)
+  //   2048 x 2048 x 1024  25 / 33 and 24 / 34    (tiled 31 / 43 and 32 / 45)
+  //   4096 x 2048 x 1024  43 / 58 and 44 / 62    (tiled 40 / 65 and 41 / 65)
+  //   4096 x 4096 x 1024  72 / 104 and 67 / 116  (tiled 57 / 104 and 58 / 104)
   // Where tiles are few and the summed index long, a wave has many slices and
   // most CUs none:
-  //   360 x 6362 x 660    dx 35 / 57             (tiled 29 / 43; 25 slices)
-  //   4096 x 512 x 512    dW 20 / 39             (tiled 21 / 32; 16 slices)
-  // float32 parts cost the tiled form more (three passes over the codes), and
-  // cost this one more where dy has to be transposed (dW).
+  //   360 x 6362 x 660    dx 35 / 46             (tiled 30 / 37; 25 slices)
+  //   4096 x 512 x 512    dW 20 / 28             (tiled 22 / 28; 16 slices)
+  // A gradient in parts costs the tiled form a pass over the codes for each,
+  // and this one more where dy has to be transposed (dW).
   p.tiles64 = ((p.rows + 63) / 64) * ((p.cols + 63) / 64);
   p.ways = 1;
   while (p.ways < 8 && p.tiles64 * p.ways * 2 <= 2048 && p.stages > p.ways) p.ways *= 2;
-  const double most = p.parts == 1 ? 6e9 : p.parts == 2 ? 18e9 : 24e9;
+  const double most = p.parts == 1 ? 5e9 : p.parts == 2 ? 8e9 : 12e9;
   p.small = n >= 8 && static_cast<double>(p.depth) * p.rows * p.cols <= most &&
             (p.tiles64 * p.ways >= 1024 || p.stages <= p.ways * (across ? 16 / p.parts : 16));
   if (p.small) {
@@ -144,15 +145,15 @@ Plan plan_of(bool across, int64_t m, int64_t n, int64_t k, int type, const void*
   }
   p.c_bytes = up(static_cast<int64_t>(p.stages) * 32 * p.ld * 2, 256);
   p.x_bytes = p.copy ? up(p.parts * p.x_pad * p.pitch * 2, 256) : 0;
-  // 256 x 256 tiles where there are enough for most of the 256 CUs; with
-  // fewer 128 x 128 tiles than CUs the summed index is split, as long as a
-  // split keeps 8 stages
+  // 256 x 256 tiles where there are enough for most of the 256 CUs; of the
+  // 128 x 128 ones a CU holds two, so with fewer than 512 the summed index is
+  // split, as long as a split keeps 16 stages
   const int64_t big = ((p.rows + 255) / 256) * ((p.cols + 255) / 256);
   p.tile = big >= 192 ? 256 : 128;
   const int64_t tiles = ((p.rows + p.tile - 1) / p.tile) * ((p.cols + p.tile - 1) / p.tile);
   const int64_t total = static_cast<int64_t>(p.stages) * p.parts;
-  int64_t splits = 256 / (tiles < 1 ? 1 : tiles);
-  if (splits > total / 8) splits = total / 8;
+  int64_t splits = p.tile == 256 ? 1 : 512 / (tiles < 1 ? 1 : tiles);
+  if (splits > total / 16) splits = total / 16;
   if (splits < 1) splits = 1;
   p.per_split = static_cast<int>((total + splits - 1) / splits);
   p.splits = p.per_split > 0 ? static_cast<int>((total + p.per_split - 1) / p.per_split) : 1;

@@ -1,0 +1,93 @@
+"""Training a linear head from preferences in mixed precision: the layer's
+operators and the preference loss of :mod:`.binding` in one SGD step.
+
+    logits = Q4(H) W4^T          W in 4 bits, H quantised in the call
+    checkpoint = Q8(H)           what the backward pass keeps of H
+    loss of the pairs, dlogits   against a frozen reference head
+    dH = dlogits W4              for the layers below, if asked for
+    W -= eta dlogits^T Q8(H)     float32 master weights, requantised
+
+    python -m communication_avoiding_mixed_amd.head [--steps N]
+
+runs it on synthetic pairs and prints the loss and accuracy of the margins.
+"""
+
+from __future__ import annotations
+
+import argparse
+
+import torch
+
+from . import binding as B
+
+
+class PreferenceHead:
+    """A head of `vocab` outputs over `features` inputs with float32 master
+    weights [vocab, features] on the GPU, tuned from pairs of sequences.
+
+    The reference head is a copy of the weights given, in the same 4 bits.
+    """
+
+    def __init__(self, weight, beta: float = 0.1, loss: str = "logistic", smoothing: float = 0.0, average: bool = False):
+        if weight.dtype != torch.float32:
+            raise ValueError("weight must be float32")
+        self.weight = weight
+        self.beta, self.loss, self.smoothing, self.average = beta, loss, smoothing, average
+        self.w4 = B.mx_quantize(weight, "mx4")
+        self.reference = self.w4
+
+    def logits(self, features):
+        """Logits of each row of features; also the single-token form."""
+        return B.mx4_linear(features, self.w4)
+
+    def reference_logps(self, features, labels):
+        """The reference head's log probabilities of the labels (once per batch)."""
+        return B.token_logps(B.mx4_linear(features, self.reference), labels)
+
+    def step(self, features, labels, offsets, ref_logps, eta: float, need_dfeatures: bool = False):
+        """One SGD step on the mean loss of the pairs (see binding.pref_loss for
+        labels and offsets).  Returns the loss's result and d loss / d features (or None)."""
+        z = self.logits(features)
+        checkpoint = B.mx_quantize(features, "mx8")
+        fwd = B.pref_loss(z, labels, offsets, ref_logps, self.beta, self.loss, self.smoothing, self.average)
+        g = torch.full((fwd.pairs,), 1.0 / fwd.pairs, device=z.device)
+        dz = B.pref_grad(fwd, g, out=z)  # the logits are not needed again
+        dh = B.mx4_grad_input(dz, self.w4) if need_dfeatures else None
+        self.weight.add_(B.mx8_grad_weight(dz, checkpoint), alpha=-eta)
+        self.w4 = B.mx_quantize(self.weight, "mx4")
+        return fwd, dh
+
+
+def synthetic_pairs(pairs: int, length: int, features: int, vocab: int, seed: int = 0):
+    """(features bf16, labels, offsets): each pair has one prompt and two
+    answers; chosen answers take their words from the lower half of the vocabulary."""
+    gen = torch.Generator().manual_seed(seed)
+    tokens = 2 * pairs * length
+    h = torch.randn(tokens, features, generator=gen)
+    labels = torch.randint(0, vocab // 2, (2 * pairs, length), generator=gen)
+    labels[1::2] += vocab - vocab // 2
+    labels[:, :length // 4] = -100  # the prompt
+    offsets = torch.arange(2 * pairs + 1) * length
+    return h.bfloat16().cuda(), labels.view(-1).cuda(), offsets.cuda()
+
+
+def main():
+    ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
+    ap.add_argument("--steps", type=int, default=20)
+    ap.add_argument("--pairs", type=int, default=16)
+    ap.add_argument("--length", type=int, default=64)
+    ap.add_argument("--features", type=int, default=2000)
+    ap.add_argument("--vocab", type=int, default=8192)
+    ap.add_argument("--eta", type=float, default=0.05)
+    a = ap.parse_args()
+    h, labels, offsets = synthetic_pairs(a.pairs, a.length, a.features, a.vocab)
+    gen = torch.Generator().manual_seed(1)
+    head = PreferenceHead((torch.randn(a.vocab, a.features, generator=gen) / a.features ** 0.5).cuda())
+    ref = head.reference_logps(h, labels)
+    for k in range(a.steps):
+        fwd, _ = head.step(h, labels, offsets, ref, a.eta)
+        print(f"step {k}: loss {float(fwd.loss.mean()):.4f}  pairs won {float((fwd.margin > 0).float().mean()):.2f}", flush=True)
+
+
+if __name__ == "__main__":
+    main()
