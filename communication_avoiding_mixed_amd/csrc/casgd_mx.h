@@ -68,11 +68,18 @@ struct Raw8 {
   u32x4 w[TY == kF32 ? 2 : 1];
 };
 
-template <int TY>
+// STREAM: loads that leave the caches to what is read again
+template <int TY, bool STREAM = false>
 __device__ __forceinline__ Raw8<TY> load_raw8(const typename Elem<TY>::type* p) {
   Raw8<TY> r;
-  r.w[0] = *reinterpret_cast<const u32x4_any*>(p);
-  if constexpr (TY == kF32) r.w[1] = *reinterpret_cast<const u32x4_any*>(p + 4);
+#pragma unroll
+  for (int i = 0; i < (TY == kF32 ? 2 : 1); ++i) {
+    const auto* q = reinterpret_cast<const u32x4_any*>(p + 4 * i);
+    if constexpr (STREAM)
+      r.w[i] = __builtin_nontemporal_load(q);
+    else
+      r.w[i] = *q;
+  }
   return r;
 }
 
@@ -91,10 +98,10 @@ __device__ __forceinline__ void widen8(const Raw8<TY>& r, float v[8]) {
 }
 
 // 8 elements from column c of a row of `cols`; zeros past its end
-template <int TY>
+template <int TY, bool STREAM = false>
 __device__ __forceinline__ void load8(const typename Elem<TY>::type* row, int64_t c, int64_t cols, float v[8]) {
   if (c + 8 <= cols) {
-    widen8<TY>(load_raw8<TY>(row + c), v);
+    widen8<TY>(load_raw8<TY, STREAM>(row + c), v);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? load1<TY>(row + c + i) : 0.f;

@@ -8,7 +8,8 @@ namespace casgd {
 namespace mx {
 namespace {
 
-constexpr int64_t kMaxDepth = int64_t{1} << 24;  // 256 rows of codes stay below 2^32 bytes
+constexpr int64_t kMaxDepth = int64_t{1} << 24;    // 256 rows of codes stay below 2^32 bytes
+constexpr int64_t kMaxOutputs = int64_t{1} << 26;  // a launch's lanes stay below 2^32
 
 // The one-launch forms quantise x again in every workgroup, which costs less
 // than a launch of its own where a wave's share of it is small.
@@ -117,6 +118,7 @@ int casgd_mx4_linear(const void* x, int x_type, int64_t m, int64_t k, int64_t x_
   if (const char* why = mx::bad_matrix(m, n, y_stride, y_type)) return api_fail(CASGD_EINVAL, why);
   if (const char* why = mx::bad_codes(w_codes, w_scales, n, mx::kMx4)) return api_fail(CASGD_EINVAL, why);
   if (k > mx::kMaxDepth) return api_fail(CASGD_EINVAL, "k exceeds 2^24");
+  if (n > mx::kMaxOutputs) return api_fail(CASGD_EINVAL, "n exceeds 2^26");
   if (m == 0) return CASGD_OK;
   const int64_t need = casgd_mx4_linear_workspace(m, k, n);
   if (!x || !y || (need > 0 && !workspace)) return api_fail(CASGD_EINVAL, "NULL pointer");

@@ -364,6 +364,8 @@ int casgd_pref_grad(const void* logits, int type, int64_t tokens, int64_t vocab,
   if (const char* why = mx::bad_matrix(tokens, vocab, out_stride, type)) return api_fail(CASGD_EINVAL, why);
   if (pairs < 1 || pairs > mx::kMaxTokens) return api_fail(CASGD_EINVAL, "pairs out of range");
   if (tokens == 0) return CASGD_OK;
+  if (dlogits == logits && out_stride != stride)
+    return api_fail(CASGD_EINVAL, "a gradient in place of the logits needs their stride");
   if (!offsets || !stats || !slope || !grad_loss || !dlogits) return api_fail(CASGD_EINVAL, "NULL pointer");
   if (reinterpret_cast<uintptr_t>(stats) % 8 != 0) return api_fail(CASGD_EINVAL, "stats must be 8-byte aligned");
   hipStream_t stream = static_cast<hipStream_t>(hip_stream);

@@ -334,7 +334,8 @@ int casgd_peak_mfma(float* out, int workgroups, int iters, void* hip_stream);
  * max |x| / scale is at most 6 (MX4) or 448 (MX8), as the fp8 storage's
  * exponent is chosen per matrix; elements are rounded to nearest even and
  * never saturate.  A block that holds a NaN or an infinity has scale byte 255
- * and stands for NaN.  codes must be 16-byte aligned, scales 4-byte.
+ * and stands for NaN; byte 0 is never written, and a block that has it may be
+ * taken as zeros.  codes must be 16-byte aligned, scales 4-byte.
  */
 enum casgd_mx_format { CASGD_MX4 = 0, CASGD_MX8 = 1 };
 
@@ -351,7 +352,7 @@ int casgd_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int format,
 
 /* y = Q4(x) W^T: x (m x k) is quantised to MX4 as by casgd_mx_quantize, W
  * (n x k) is kept in MX4; float32 sums, rounded once to y's type (m x n).
- * k <= 2^24.  workspace: casgd_mx4_linear_workspace(m, k, n) bytes at
+ * k <= 2^24, n <= 2^26.  workspace: casgd_mx4_linear_workspace(m, k, n) bytes at
  * least (0: none), 16-byte aligned, free again when the call's work is done.
  * Bit-identical on repeats. */
 int64_t casgd_mx4_linear_workspace(int64_t m, int64_t k, int64_t n);
@@ -406,6 +407,7 @@ int casgd_token_logps(const void* logits, int type, int64_t tokens, int64_t voca
  *              gradient (max and 1 / sum of the row's softmax)
  *   slope      device, float32 [2 pairs]: d loss / d logps of each sequence
  *   workspace  casgd_pref_workspace(tokens) bytes, 8-byte aligned
+ * tokens and pairs are below 2^23.
  * Sums over tokens are float64 in a fixed order.
  */
 int64_t casgd_pref_workspace(int64_t tokens);

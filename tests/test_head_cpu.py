@@ -54,6 +54,9 @@ def test_product_refusals():
     linear(0, None, "NULL"), linear(8, None, "NULL"), linear(11, None, "NULL"), linear(5, None, "NULL")
     linear(1, 3, "element type"), linear(9, 7, "element type"), linear(4, 63, "row stride"), linear(10, 7, "row stride")
     linear(12, need - 1, "workspace"), linear(11, ODD, "aligned"), linear(5, ODD, "aligned"), linear(7, 0, "columns")
+    linear(7, 2 ** 27, "row stride")
+    refused(lib.casgd_mx4_linear(P, B.BF16, 4, 64, 64, P, P, 2 ** 27, P, B.BF16, 2 ** 27, P, need, None), "2^26")
+    refused(lib.casgd_mx4_linear(P, B.BF16, 4, 2 ** 25, 2 ** 25, P, P, 8, P, B.BF16, 8, P, need, None), "2^24")
 
 
 def test_gradient_refusals():
@@ -105,6 +108,7 @@ def test_preference_refusals():
     refused(lib.casgd_token_logps(P, B.FP32, 6, 9, 9, P, None, None), "NULL")
     refused(lib.casgd_pref_grad(P, B.FP32, 6, 9, 9, P, P, 1, P, P, None, P, 9, None), "NULL")
     refused(lib.casgd_pref_grad(P, B.FP32, 6, 9, 9, P, P, 1, P, P, P, P, 8, None), "row stride")
+    refused(lib.casgd_pref_grad(P, B.FP32, 6, 9, 9, P, P, 1, P, P, P, P, 10, None), "in place")
     refused(lib.casgd_pref_grad(P, B.FP32, 6, 9, 9, P, P, 0, P, P, P, P, 9, None), "pairs")
 
 
