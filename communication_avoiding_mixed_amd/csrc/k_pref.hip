@@ -6,9 +6,9 @@
 //   squared   l = (h - 1 / (2 beta))^2
 //   dz_t[v] = g l'(h) (+-1) (1[v = y_t] - exp(z_t[v] - lse_t))
 //
-// Three launches: a row kernel (running max and sum of each row's softmax),
-// a pair kernel (float64 sums of the pair's tokens in a fixed order) and the
-// gradient's row kernel.  The rows are read twice and written once, since a
+// Three launches (two for few short rows): a row kernel (running max and sum of
+// each row's softmax), a pair kernel (float64 sums of the pair's tokens in a
+// fixed order) and the gradient's row kernel.  The rows are read twice and written once, since a
 // pair's slope needs all of its rows; both row kernels are bound by that
 // traffic.
 #include "casgd.h"
@@ -54,30 +54,11 @@ __device__ __forceinline__ void load_logits(const typename Elem<TY>::type* row, 
   }
 }
 
-// LANES lanes per row (64: a wave each of the workgroup's 256 lanes; 256 or
-// 1024: the workgroup), four 16-byte loads of a lane in flight.  NaN: the max
-// drops NaN operands, but exp(NaN - m) in the sum keeps it.
+// The running max and sum of a row's softmax, joined over the wave, from the
+// pieces that lane `lane` of LANES takes; four 16-byte loads in flight.  NaN:
+// the max drops NaN operands, but exp(NaN - m) in the sum keeps it.
 template <int TY, int LANES>
-__global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void row_stats_kernel(
-    const typename Elem<TY>::type* __restrict__ logits, int64_t tokens, int64_t vocab, int64_t stride,
-    const int64_t* __restrict__ labels, float* __restrict__ logps, double* __restrict__ logps64, float2* __restrict__ stats) {
-  constexpr int WAVES = LANES / 64;
-  __shared__ MaxSum part[WAVES];
-  const int64_t t = LANES == 64 ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
-  if (t >= tokens) return;
-  const int lane = threadIdx.x % LANES;
-  const int64_t label = labels[t];
-  if (label < 0) {
-    if (lane == 0) {
-      logps[t] = 0.f;
-      if (logps64) logps64[t] = 0.0;
-      if (stats) stats[t] = make_float2(0.f, 1.f);
-    }
-    return;
-  }
-  const auto* row = logits + t * stride;
-  // a label past the vocabulary is not read: its row becomes NaN
-  const float z = label < vocab ? load1<TY>(row + label) : NAN;
+__device__ __forceinline__ MaxSum row_max_sum(const typename Elem<TY>::type* row, int64_t vocab, int lane) {
   MaxSum acc = {-INFINITY, 0.f};
   constexpr int UNROLL = 4;
   for (int64_t c = static_cast<int64_t>(lane) * 8; c < vocab; c += UNROLL * LANES * 8) {
@@ -101,6 +82,38 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void row_stats_kernel(
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) acc = join(acc, MaxSum{__shfl_xor(acc.m, o, 64), __shfl_xor(acc.s, o, 64)});
+  return acc;
+}
+
+// The label's log probability in float64, from its logit and the row's sums
+__device__ __forceinline__ double log_prob(float z, MaxSum acc) {
+  return (static_cast<double>(z) - acc.m) - log(static_cast<double>(acc.s));
+}
+
+// LANES lanes per row: 64, a wave each of the workgroup's 256 lanes; 256 or
+// 1024, the workgroup.
+template <int TY, int LANES>
+__global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void row_stats_kernel(
+    const typename Elem<TY>::type* __restrict__ logits, int64_t tokens, int64_t vocab, int64_t stride,
+    const int64_t* __restrict__ labels, float* __restrict__ logps, double* __restrict__ logps64, float2* __restrict__ stats) {
+  constexpr int WAVES = LANES / 64;
+  __shared__ MaxSum part[WAVES];
+  const int64_t t = LANES == 64 ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  if (t >= tokens) return;
+  const int lane = threadIdx.x % LANES;
+  const int64_t label = labels[t];
+  if (label < 0) {
+    if (lane == 0) {
+      logps[t] = 0.f;
+      if (logps64) logps64[t] = 0.0;
+      if (stats) stats[t] = make_float2(0.f, 1.f);
+    }
+    return;
+  }
+  const auto* row = logits + t * stride;
+  // a label past the vocabulary is not read: its row becomes NaN
+  const float z = label < vocab ? load1<TY>(row + label) : NAN;
+  MaxSum acc = row_max_sum<TY, LANES>(row, vocab, lane);
   if constexpr (WAVES > 1) {
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = acc;
     __syncthreads();
@@ -109,13 +122,48 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void row_stats_kernel(
       for (int w = 1; w < WAVES; ++w) acc = join(acc, part[w]);
   }
   if (lane != 0) return;
-  const double lp = (static_cast<double>(z) - acc.m) - log(static_cast<double>(acc.s));
+  const double lp = log_prob(z, acc);
   logps[t] = static_cast<float>(lp);
   if (logps64) logps64[t] = lp;
   if (stats) stats[t] = make_float2(acc.m, 1.f / acc.s);
 }
 
 __device__ __forceinline__ int64_t clamp_row(int64_t r, int64_t tokens) { return r < 0 ? 0 : r > tokens ? tokens : r; }
+
+// A pair's loss, margin and slopes from its waves' sums and counts (chosen,
+// then rejected), added in order.
+__device__ void finish_pair(const double* sums, const double* counts, int waves, int64_t p, int kind, float beta,
+                            float smoothing, int average, float* loss, float* margin, float* slope) {
+  double mean[2], per[2];
+#pragma unroll
+  for (int d = 0; d < 2; ++d) {
+    double s = 0.0, n = 0.0;
+    for (int w = 0; w < waves; ++w) {
+      s += sums[d * waves + w];
+      n += counts[d * waves + w];
+    }
+    per[d] = average && n > 1.0 ? 1.0 / n : 1.0;
+    mean[d] = s * per[d];
+  }
+  const double h = mean[0] - mean[1], bt = beta, eps = smoothing;
+  double l, d;
+  if (kind == kLogistic) {
+    const double u = bt * h;
+    const double e = exp(-fabs(u));
+    const double sig_neg = u >= 0.0 ? e / (1.0 + e) : 1.0 / (1.0 + e);  // logistic function of -u
+    // a term of weight zero is left out, so that an infinite u keeps a finite loss
+    l = (eps < 1.0 ? (1.0 - eps) * loss_value<kLogistic>(u, 1.0) : 0.0) + (eps > 0.0 ? eps * loss_value<kLogistic>(u, -1.0) : 0.0);
+    d = bt * (eps - sig_neg);
+  } else {
+    const double r = h - 0.5 / bt;
+    l = r * r;
+    d = 2.0 * r;
+  }
+  loss[p] = static_cast<float>(l);
+  margin[p] = static_cast<float>(h);
+  slope[2 * p] = static_cast<float>(d * per[0]);
+  slope[2 * p + 1] = static_cast<float>(-d * per[1]);
+}
 
 // One workgroup per pair, half of its waves for each side: a lane sums its
 // tokens in float64, then lanes and waves join in a fixed order.
@@ -158,36 +206,62 @@ __global__ __launch_bounds__(2 * kThreads) void pair_kernel(const double* __rest
   }
   __syncthreads();
   if (threadIdx.x != 0) return;
-  double mean[2], per[2];
-#pragma unroll
-  for (int d = 0; d < 2; ++d) {
-    s = n = 0.0;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      s += sums[d * kWaves + w];
-      n += counts[d * kWaves + w];
+  finish_pair(sums, counts, kWaves, p, kind, beta, smoothing, average, loss, margin, slope);
+}
+
+// The whole loss in one launch, for few short rows: a workgroup per pair, a row
+// a wave at a time.  Rows of no pair go to the first and the last workgroup.
+template <int TY>
+__global__ __launch_bounds__(1024) void pair_rows_kernel(const typename Elem<TY>::type* __restrict__ logits, int64_t tokens,
+                                                        int64_t vocab, int64_t stride, const int64_t* __restrict__ labels,
+                                                        const int64_t* __restrict__ offsets, const float* __restrict__ ref,
+                                                        int kind, float beta, float smoothing, int average,
+                                                        float* __restrict__ loss, float* __restrict__ margin,
+                                                        float* __restrict__ logps, float2* __restrict__ stats,
+                                                        float* __restrict__ slope) {
+  constexpr int WAVES = 16;
+  __shared__ double sums[2 * WAVES], counts[2 * WAVES];
+  const int64_t p = blockIdx.x;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t start = clamp_row(offsets[2 * p], tokens), middle = clamp_row(offsets[2 * p + 1], tokens),
+                stop = clamp_row(offsets[2 * p + 2], tokens);
+  double s[2] = {0.0, 0.0}, n[2] = {0.0, 0.0};
+  const int64_t first = p == 0 ? 0 : start, last = p + 1 == static_cast<int64_t>(gridDim.x) ? tokens : stop;
+  for (int64_t t = first + wave; t < last; t += WAVES) {
+    const int64_t label = labels[t];
+    double lp = 0.0;
+    float2 st = make_float2(0.f, 1.f);
+    if (label >= 0) {
+      const auto* row = logits + t * stride;
+      const float z = label < vocab ? load1<TY>(row + label) : NAN;
+      const MaxSum acc = row_max_sum<TY, 64>(row, vocab, lane);
+      lp = log_prob(z, acc);
+      st = make_float2(acc.m, 1.f / acc.s);
+      if (t >= start && t < stop) {
+        const double d = lp - (ref ? static_cast<double>(ref[t]) : 0.0);
+        if (t < middle) {
+          s[0] += d;
+          n[0] += 1.0;
+        } else {
+          s[1] += d;
+          n[1] += 1.0;
+        }
+      }
     }
-    per[d] = average && n > 1.0 ? 1.0 / n : 1.0;
-    mean[d] = s * per[d];
+    if (lane == 0) {
+      logps[t] = static_cast<float>(lp);
+      stats[t] = st;
+    }
   }
-  const double h = mean[0] - mean[1], bt = beta, eps = smoothing;
-  double l, d;
-  if (kind == kLogistic) {
-    const double u = bt * h;
-    const double e = exp(-fabs(u));
-    const double sig_neg = u >= 0.0 ? e / (1.0 + e) : 1.0 / (1.0 + e);  // logistic function of -u
-    // a term of weight zero is left out, so that an infinite u keeps a finite loss
-    l = (1.0 - eps) * loss_value<kLogistic>(u, 1.0) + (eps > 0.0 ? eps * loss_value<kLogistic>(u, -1.0) : 0.0);
-    d = bt * (eps - sig_neg);
-  } else {
-    const double r = h - 0.5 / bt;
-    l = r * r;
-    d = 2.0 * r;
+  if (lane == 0) {
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      sums[d * WAVES + wave] = s[d];
+      counts[d * WAVES + wave] = n[d];
+    }
   }
-  loss[p] = static_cast<float>(l);
-  margin[p] = static_cast<float>(h);
-  slope[2 * p] = static_cast<float>(d * per[0]);
-  slope[2 * p + 1] = static_cast<float>(-d * per[1]);
+  __syncthreads();
+  if (threadIdx.x == 0) finish_pair(sums, counts, WAVES, p, kind, beta, smoothing, average, loss, margin, slope);
 }
 
 // The sequence that holds row t: the last one whose start is at or before it.
@@ -277,6 +351,27 @@ hipError_t launch_stats(int type, const void* logits, int64_t tokens, int64_t vo
   return stats_as<kF32>(logits, tokens, vocab, stride, labels, logps, logps64, stats, stream);
 }
 
+// One launch takes the whole loss while a pair's workgroup has little to read:
+// 61 x 2000 float32 in two pairs 8.1 us of host time and no more on the device
+// (two launches 10.7), 128 x 2000 in one pair 31 us (two launches 11).  How the
+// tokens are spread over the pairs is not known here; few of them bound the
+// worst case.
+constexpr int64_t kRowsOfPairs = 128, kElementsOfPair = 65536;
+bool pairs_fit(int64_t tokens, int64_t vocab, int64_t pairs) {
+  return tokens <= kRowsOfPairs && vocab <= kWaveRow && tokens * vocab <= pairs * kElementsOfPair;
+}
+
+template <int TY>
+hipError_t pair_rows_as(const void* logits, int64_t tokens, int64_t vocab, int64_t stride, const int64_t* labels,
+                        const int64_t* offsets, int64_t pairs, const float* ref, int kind, float beta, float smoothing,
+                        int average, float* loss, float* margin, float* logps, float* stats, float* slope,
+                        hipStream_t stream) {
+  hipLaunchKernelGGL((pair_rows_kernel<TY>), dim3(static_cast<unsigned>(pairs)), dim3(1024), 0, stream,
+                     static_cast<const typename Elem<TY>::type*>(logits), tokens, vocab, stride, labels, offsets, ref, kind,
+                     beta, smoothing, average, loss, margin, logps, reinterpret_cast<float2*>(stats), slope);
+  return hipGetLastError();
+}
+
 template <int TY>
 hipError_t grad_as(const void* logits, int64_t tokens, int64_t vocab, int64_t stride, const int64_t* labels,
                    const int64_t* offsets, int64_t pairs, const float* stats, const float* slope, const float* grad_loss,
@@ -302,7 +397,7 @@ hipError_t grad_as(const void* logits, int64_t tokens, int64_t vocab, int64_t st
 }
 
 // rows are workgroups: fewer than 2^32 threads a launch
-constexpr int64_t kMaxTokens = (int64_t{1} << 32) / (2 * kThreads) - 1;
+constexpr int64_t kMaxTokens = (int64_t{1} << 32) / 1024 - 1;
 
 const char* bad_logits(const void* logits, int type, int64_t tokens, int64_t vocab, int64_t stride, const int64_t* labels) {
   if (const char* why = bad_matrix(tokens, vocab, stride, type)) return why;
@@ -347,6 +442,14 @@ int casgd_pref_loss(const void* logits, int type, int64_t tokens, int64_t vocab,
     return api_fail(CASGD_EINVAL, "stats and workspace must be 8-byte aligned");
   if (workspace_bytes < casgd_pref_workspace(tokens)) return api_fail(CASGD_EINVAL, "workspace too small");
   hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+  if (mx::pairs_fit(tokens, vocab, pairs)) {
+    const auto launch = type == mx::kBF16 ? mx::pair_rows_as<mx::kBF16>
+                        : type == mx::kF16 ? mx::pair_rows_as<mx::kF16>
+                                           : mx::pair_rows_as<mx::kF32>;
+    const hipError_t e = launch(logits, tokens, vocab, stride, labels, offsets, pairs, ref_logps, loss_kind, beta, smoothing,
+                                average, loss, margin, logps, stats, slope, stream);
+    return e == hipSuccess ? CASGD_OK : api_hip_fail(e, "preference loss launch");
+  }
   double* logps64 = static_cast<double*>(workspace);
   hipError_t e = mx::launch_stats(type, logits, tokens, vocab, stride, labels, logps, logps64, stats, stream);
   if (e == hipSuccess) {

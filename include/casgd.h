@@ -407,7 +407,7 @@ int casgd_token_logps(const void* logits, int type, int64_t tokens, int64_t voca
  *              gradient (max and 1 / sum of the row's softmax)
  *   slope      device, float32 [2 pairs]: d loss / d logps of each sequence
  *   workspace  casgd_pref_workspace(tokens) bytes, 8-byte aligned
- * tokens and pairs are below 2^23.
+ * tokens and pairs are below 2^22.
  * Sums over tokens are float64 in a fixed order.
  */
 int64_t casgd_pref_workspace(int64_t tokens);
