@@ -332,9 +332,12 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void mx4_gemm_kernel(Mx4Operand x,
 }
 
 // The waves' sums of 32 MT rows of x by 32 rows of W (from row n0), added in
-// order and stored.  part: 4 KB a wave.
+// order and stored.  part: 64 sums a row, padded by one: a row of y takes its
+// columns from 16 of them, which met in one bank (2 of 17 us at
+// 24 x 8192 x 16384).
+constexpr int kPartRow = 65;
 template <int OUT, int MT, int WAVES>
-__device__ __forceinline__ void join_waves(const f32x16 (&acc)[MT], float (*part)[16][64], typename Elem<OUT>::type* y,
+__device__ __forceinline__ void join_waves(const f32x16 (&acc)[MT], float (*part)[16][kPartRow], typename Elem<OUT>::type* y,
                                            int64_t stride, int64_t n0, int64_t m_rows, int64_t n_rows) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
@@ -463,8 +466,9 @@ __global__ __launch_bounds__(64 * WAVES) void mx4_stream_kernel(Mx4Operand x, Mx
         for (int i = 0; i < 4; ++i) acc[a][b] = mfma_mx4_32(f[a][i], f[NT + b][i], acc[a][b], sc[a], sc[NT + b], i);
     slot ^= 1;
   }
+  static_assert(16 * kPartRow * 4 <= 2 * SLOT, "a wave's sums fit its slots");
   __syncthreads();  // the slots become the waves' sums
-  auto part = reinterpret_cast<float(*)[16][64]>(smem);
+  auto part = reinterpret_cast<float(*)[16][kPartRow]>(smem);
 #pragma unroll
   for (int a = 0; a < NT; ++a) {
     if (a > 0) __syncthreads();
@@ -478,7 +482,7 @@ template <int TY, int OUT>
 __global__ __launch_bounds__(512) void mx4_fused_kernel(const typename Elem<TY>::type* __restrict__ x, int64_t m, int64_t k,
                                                        int64_t x_stride, Mx4Operand w, int64_t ld,
                                                        typename Elem<OUT>::type* __restrict__ y, int64_t stride) {
-  __shared__ float part[8][16][64];
+  __shared__ float part[8][16][kPartRow];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int half = lane >> 5, r32 = lane & 31;
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 32;
@@ -529,7 +533,7 @@ template <int TY, int OUT>
 __global__ __launch_bounds__(512) void mx4_decode_kernel(const typename Elem<TY>::type* __restrict__ x, int64_t m, int64_t k,
                                                         int64_t x_stride, Mx4Operand w, int64_t ld,
                                                         typename Elem<OUT>::type* __restrict__ y, int64_t stride) {
-  __shared__ float part[8][4][64];
+  __shared__ float part[8][4][68];  // padded, as above
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, r16 = lane & 15;
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
