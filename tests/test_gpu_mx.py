@@ -299,3 +299,32 @@ def test_binding_refusals():
         B.mx8_grad_weight(torch.zeros(4, 8, device="cuda"), B.mx_quantize(x, "mx8"), out=torch.zeros(8, 63, device="cuda"))
     with pytest.raises(ValueError, match="uint8"):
         B.MXMatrix("mx4", w.codes.to(torch.int32), w.scales, 64)
+
+
+def test_offsets_past_32_bits():
+    # 8.7 GB of bf16: byte and element offsets of the last rows pass 2^32
+    m, k = 66001, 65536
+    x = torch.zeros((m, k), dtype=torch.bfloat16, device="cuda")
+    tail = cuda(values((3, k), 1), "bf16")
+    x[-3:] = tail
+    codes, scales = H.quantize(host(tail), "mx8")
+    q = B.mx_quantize(x, "mx8")
+    np.testing.assert_array_equal(q.codes[-3:].cpu().numpy(), codes)
+    np.testing.assert_array_equal(q.scales[-3:].cpu().numpy(), scales)
+    assert torch.equal(B.mx_dequantize(q, torch.bfloat16)[-3:].double().cpu(),
+                       torch.from_numpy(H.dequantize(codes, scales, k, "mx8")).bfloat16().double())
+    del q
+    w = stored(values((40, k), 2) / 256, "mx4")
+    wv = H.dequantize(w.codes.cpu().numpy(), w.scales.cpu().numpy(), k, "mx4")
+    y = B.mx4_linear(x, w)
+    close(y[-3:], H.rounded(host(tail), "mx4"), wv.T, "bf16")
+    assert not y[:-3].any()
+    # x as a gradient of k outputs: dW's rows are its columns, dx's its rows
+    act = torch.zeros((m, 40), device="cuda")
+    act[-3:] = cuda(values((3, 40), 3))
+    dw = B.mx8_grad_weight(x, B.mx_quantize(act, "mx8"))
+    close(dw[-100:], host(tail[:, -100:]).T, H.rounded(host(act[-3:]), "mx8"), "fp32")
+    wide = stored(values((k, 40), 4) / 256, "mx4")
+    dx = B.mx4_grad_input(x, wide)
+    close(dx[-3:], host(tail), H.dequantize(wide.codes.cpu().numpy(), wide.scales.cpu().numpy(), 40, "mx4"), "bf16")
+    assert not dx[:-3].any()

@@ -276,3 +276,24 @@ def test_binding_refusals():
         B.pref_grad(fwd, gpu(g), out=torch.zeros(6, 41, device="cuda"))
     with pytest.raises(ValueError, match="out must"):
         B.pref_grad(fwd, gpu(g), out=torch.zeros(6, 40, device="cuda", dtype=torch.float16))
+
+
+def test_offsets_past_32_bits():
+    # 8.7 GB of bf16 logits; only the last rows are labelled, the others are not read
+    tokens, vocab = 66001, 65536
+    z = torch.empty((tokens, vocab), dtype=torch.bfloat16, device="cuda")
+    tail = torch.randn(4, vocab, device="cuda").bfloat16()
+    z[-4:] = tail
+    labels = torch.full((tokens,), -1, dtype=torch.int64)
+    labels[-4:] = torch.tensor([vocab - 1, 5, 77, vocab - 2])
+    offsets = torch.tensor([0, tokens - 2, tokens])
+    fwd = B.pref_loss(z, labels.cuda(), offsets.cuda())
+    lp = H.token_logps(host(tail), labels[-4:].numpy())
+    np.testing.assert_allclose(host(fwd.logps[-4:]), lp, rtol=3e-6)
+    d = B.pref_grad(fwd, torch.ones(1, device="cuda"))
+    small = B.pref_loss(tail, labels[-4:].cuda(), torch.tensor([0, 2, 4]).cuda())
+    assert abs(float(fwd.loss) - float(small.loss)) <= 1e-5
+    ref = host(B.pref_grad(small, torch.ones(1, device="cuda")))
+    # the two calls' sums run in another order: slopes and softmax differ by a few float32 steps, then bf16's
+    assert (np.abs(host(d[-4:]) - ref) <= 2.0 ** -7 * np.abs(ref) + 1e-12).all()
+    assert not d[:-4].any()
