@@ -52,6 +52,10 @@ constexpr int grad_lds_bytes() {
 // The four rows' 64 bytes that 32 lanes read in a cycle would meet in the same
 // banks, so row t's 16-byte pieces are stored at piece XOR 4 (t mod 4).  A matrix whose rows are the
 // output is staged as 64 bytes of each row, as the 4-bit product's codes are.
+//
+// 256 x 256 by 8 waves, 4096 x 8192 x 4096: dx 260 us, dW 272 us, 1.06 and 1.01
+// PFLOP/s.  The matrix instructions alone take 173 and 190 us on such data (the
+// clock falls under them), without loads the kernel takes 202 and 220.
 template <int OUT, bool ACROSS, int RX, int RC, int GM, int GN>
 __global__ __launch_bounds__(64 * GM * GN, 2) void mx_grad_kernel(GradArgs g, typename Elem<OUT>::type* __restrict__ out_,
                                                                  int64_t stride, int64_t split_stride, int accumulate) {

@@ -11,6 +11,16 @@ namespace {
 constexpr int64_t kMaxDepth = int64_t{1} << 24;    // 256 rows of codes stay below 2^32 bytes
 constexpr int64_t kMaxOutputs = int64_t{1} << 26;  // a launch's lanes stay below 2^32
 
+// Rows of x that the streaming form takes, and, beyond 64 of them, how many
+// 128 x 128 tiles at most and how long a summed index at least: few tiles leave
+// most CUs idle for the length of k, where the streaming form's 8 workgroups
+// for each share it.  us, streaming and tiled:
+//   84 x 7858 x 566    12 and 29     128 x 4096 x 4096  11 and 18
+//   512 x 4096 x 1024  12 and 18     256 x 4096 x 4096  15 and 18 (64 tiles)
+//   256 x 8192 x 8192  42 and 31 (128 tiles)
+//   512 x 512 x 512    13 and 11
+constexpr int64_t kStreamRows = 1024, kFewTiles = 64, kLongIndex = 2048;
+
 // The one-launch forms quantise x again in every workgroup, which costs less
 // than a launch of its own where a wave's share of it is small.
 //   16 rows a workgroup:  16 x 4096 x 4096 11.5 us (two launches 12.7),
@@ -42,8 +52,9 @@ hipError_t stream_as(const Mx4Operand& x, const Mx4Operand& w, int64_t ld, typen
   static const hipError_t allowed =
       hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (allowed != hipSuccess) return allowed;
-  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>((w.rows + 32 * NT - 1) / (32 * NT))), dim3(64 * WAVES), lds, stream, x,
-                     w, ld, y, stride);
+  const dim3 grid(static_cast<unsigned>((w.rows + 32 * NT - 1) / (32 * NT)),
+                  static_cast<unsigned>((x.rows + 32 * MT - 1) / (32 * MT)));
+  hipLaunchKernelGGL(kernel, grid, dim3(64 * WAVES), lds, stream, x, w, ld, y, stride);
   return hipGetLastError();
 }
 
@@ -55,7 +66,8 @@ hipError_t product_as(const Mx4Operand& x, const Mx4Operand& w, int64_t ld, void
   const bool wide = w.rows >= 64 * 192;
   if (x.rows <= 32)
     return wide ? stream_as<OUT, 2, 1, 4>(x, w, ld, out, stride, stream) : stream_as<OUT, 1, 1, 8>(x, w, ld, out, stride, stream);
-  if (x.rows <= 64)
+  const int64_t tiles = ((x.rows + 127) / 128) * ((w.rows + 127) / 128);
+  if (x.rows <= 64 || (x.rows <= kStreamRows && tiles <= kFewTiles && ld >= kLongIndex))
     return wide ? stream_as<OUT, 2, 2, 4>(x, w, ld, out, stride, stream) : stream_as<OUT, 1, 2, 4>(x, w, ld, out, stride, stream);
   // the large tile moves half the bytes per product; it needs one for every CU
   if (((x.rows + 255) / 256) * ((w.rows + 255) / 256) >= 256) return gemm_as<OUT, 256, 256, 4, 2>(x, w, ld, y, stride, stream);

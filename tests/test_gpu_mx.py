@@ -109,7 +109,8 @@ def test_quantise_ties_extremes_and_non_finite_blocks(fmt):
 LINEAR = [(1, 1, 1), (1, 32, 5), (1, 2000, 300), (2, 129, 64), (5, 640, 33), (15, 4096, 17), (16, 512, 16), (17, 96, 130),
           (31, 256, 257), (33, 1000, 128), (64, 128, 64), (65, 160, 300), (100, 2000, 259), (128, 512, 256),
           (129, 700, 127), (257, 384, 513), (300, 64, 1024),
-          (16, 8200, 2100), (24, 2300, 300), (31, 4000, 40), (7, 2560, 12400), (32, 2176, 12289), (20, 9000, 33), (60, 3000, 200)]
+          (16, 8200, 2100), (24, 2300, 300), (31, 4000, 40), (7, 2560, 12400), (32, 2176, 12289), (20, 9000, 33), (60, 3000, 200),
+          (65, 2048, 40), (150, 2500, 100), (1000, 2100, 50), (1030, 2100, 50)]
 
 
 @pytest.mark.parametrize("m,k,n", LINEAR)
