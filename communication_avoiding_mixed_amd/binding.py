@@ -305,7 +305,8 @@ def unpack_gram(G_packed: np.ndarray, s: int, b: int) -> dict:
 # the stream is taken as the raw handle.
 
 _TYPES = {torch.bfloat16: BF16, torch.float32: FP32, torch.float16: FP16}
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+# the current stream's handle without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current_device = torch.cuda.current_device
 
 

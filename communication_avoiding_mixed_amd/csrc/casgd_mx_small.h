@@ -21,14 +21,16 @@ __device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return
 
 // v[0 .. 7] as PARTS bf16 vectors that sum to it exactly: each keeps the 8
 // leading bits of what is left, cut towards zero so that none overflows; a
-// value that is not finite is its first part.  Vectors with such a value take
-// a branch of their own.
+// value that is not finite is its first part.  Vectors with an infinity take a
+// branch of their own.
 template <int PARTS>
 __device__ __forceinline__ void split8(float v[8], u32x4 (&out)[PARTS]) {
-  uint32_t top = 0;
+  // The max leaves NaN out: in the other branch a NaN's first rest is a NaN, and
+  // so is its second part.
+  float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max_u32(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  if (top >= 0x7F800000u) {
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
+  if (top == INFINITY) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t bits = __float_as_uint(v[i]);

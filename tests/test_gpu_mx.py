@@ -329,3 +329,19 @@ def test_offsets_past_32_bits():
     dx = B.mx4_grad_input(x, wide)
     close(dx[-3:], host(tail), H.dequantize(wide.codes.cpu().numpy(), wide.scales.cpu().numpy(), 40, "mx4"), "bf16")
     assert not dx[:-3].any()
+
+
+@pytest.mark.parametrize("shape", [(70, 90, 100), (2500, 2600, 2100)])
+def test_gradient_parts_keep_infinities_and_every_nan(shape):
+    # the one-launch and the tiled form; a NaN whose set bits are the lowest, infinities of both signs
+    m, n, k = shape
+    w, x = stored(np.ones((n, k), np.float32), "mx4"), stored(np.ones((m, k), np.float32), "mx8")
+    for dtype, word in (("fp32", 0x7F800001), ("fp16", 0x7C01)):
+        dy = torch.ones((m, n), dtype=T[dtype], device="cuda")
+        dy[3, 4], dy[5, 6] = float("inf"), float("-inf")
+        bits = dy.view(torch.int32 if dtype == "fp32" else torch.int16)
+        bits[8, 9] = word
+        dx, dw = host(B.mx4_grad_input(dy, w)), host(B.mx8_grad_weight(dy, x))
+        assert (dx[3] == np.inf).all() and (dx[5] == -np.inf).all() and np.isnan(dx[8]).all()
+        assert (dw[4] == np.inf).all() and (dw[6] == -np.inf).all() and np.isnan(dw[9]).all()
+        assert np.isfinite(np.delete(dx, [3, 5, 8], 0)).all() and np.isfinite(np.delete(dw, [4, 6, 9], 0)).all()
