@@ -10,8 +10,8 @@
 // each row's softmax), a pair kernel (float64 sums of the pair's tokens in a
 // fixed order) and the gradient's row kernel.  The rows are read twice and
 // written once, since a pair's slope needs all of its rows; both row kernels are
-// bound by that traffic.  8192 x 65536 bf16, a quarter of the rows masked: 129 us
-// (805 MB, part of it still in the last-level cache), 8 us and 336 us (5.6 TB/s).
+// bound by that traffic.  8192 x 65536 bf16, a quarter of the rows masked: 126 us
+// (805 MB, part of it still in the last-level cache), 8 us and 294 us (6.4 TB/s).
 #include "casgd.h"
 #include "casgd_internal.h"
 #include "casgd_mx.h"
@@ -280,10 +280,10 @@ __device__ __forceinline__ int64_t sequence_of(const int64_t* offsets, int64_t s
 }
 
 // Rows from the last to the first: the loss read them in the other order, so
-// its last ones are still in the last-level cache (8192 x 65536 bf16: 336 us,
-// from the first 366 us).  STREAM keeps the gradient out of that cache.
+// its last ones are still in the last-level cache (8192 x 65536 bf16, 256
+// lanes a row: 336 us, from the first 366 us).  STREAM keeps the gradient out of that cache.
 template <int TY, bool STREAM, int LANES>
-__global__ __launch_bounds__(kThreads) void row_grad_kernel(const typename Elem<TY>::type* logits, int64_t tokens,
+__global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void row_grad_kernel(const typename Elem<TY>::type* logits, int64_t tokens,
                                                            int64_t vocab, int64_t stride, const int64_t* __restrict__ labels,
                                                            const int64_t* __restrict__ offsets, int64_t sequences,
                                                            const float2* __restrict__ stats, const float* __restrict__ slope,
@@ -323,9 +323,14 @@ __global__ __launch_bounds__(kThreads) void row_grad_kernel(const typename Elem<
   }
 }
 
-// Few long rows get workgroups of 1024 lanes, so that a row is a few rounds of
-// loads; rows that a wave reads in two rounds get a wave; 256 lanes otherwise.
-constexpr int64_t kFewTokens = 512, kLongRow = 8192, kWaveRow = 4096;
+// Lanes per row.  Few long rows get workgroups of 1024, so that a row is a few
+// rounds of loads (38 x 20311: gradient 7.2 us, with 256 lanes 9.7); rows that a
+// wave reads in two rounds get a wave (8192 x 256: loss 20 us, with 256 lanes
+// 29); very long ones more lanes, so that fewer rows stream at once, with inputs
+// from memory: 8192 x 65536 gradient 366 us with 1024, 397 with 512, 415 with
+// 256, loss 184 with 512, 194 with 256; 2048 x 32768 gradient 50 and 53.  Others
+// 256: 8192 x 16384 loss 54 us, with 512 65, gradient 94, with 1024 120.
+constexpr int64_t kFewTokens = 512, kLongRow = 8192, kWaveRow = 4096, kWideGradRow = 32768, kWideLossRow = 65536;
 
 template <int TY>
 hipError_t stats_as(const void* logits, int64_t tokens, int64_t vocab, int64_t stride, const int64_t* labels, float* logps,
@@ -335,6 +340,9 @@ hipError_t stats_as(const void* logits, int64_t tokens, int64_t vocab, int64_t s
   if (tokens <= kFewTokens && vocab >= kLongRow)
     hipLaunchKernelGGL((row_stats_kernel<TY, 1024>), dim3(static_cast<unsigned>(tokens)), dim3(1024), 0, stream, z, tokens,
                        vocab, stride, labels, logps, logps64, st);
+  else if (vocab >= kWideLossRow)
+    hipLaunchKernelGGL((row_stats_kernel<TY, 512>), dim3(static_cast<unsigned>(tokens)), dim3(512), 0, stream, z, tokens, vocab,
+                       stride, labels, logps, logps64, st);
   else if (vocab <= kWaveRow)
     hipLaunchKernelGGL((row_stats_kernel<TY, 64>), dim3(static_cast<unsigned>((tokens + 3) / 4)), dim3(kThreads), 0, stream, z,
                        tokens, vocab, stride, labels, logps, logps64, st);
@@ -380,20 +388,19 @@ hipError_t grad_as(const void* logits, int64_t tokens, int64_t vocab, int64_t st
   const auto* z = static_cast<const typename Elem<TY>::type*>(logits);
   auto* out = static_cast<typename Elem<TY>::type*>(dlogits);
   const auto* st = reinterpret_cast<const float2*>(stats);
-  const dim3 block(kThreads);
   // Half of the 256 MB last-level cache: a gradient that is larger would push
   // out the logits that are still to be read (the loss's next pass over
   // 8192 x 65536 bf16 135 us instead of 167); a smaller one stays for its reader.
   const bool large = tokens * vocab * static_cast<int64_t>(sizeof(*z)) >= (int64_t{1} << 27);
-  if (vocab <= kWaveRow && !large)
-    hipLaunchKernelGGL((row_grad_kernel<TY, false, 64>), dim3(static_cast<unsigned>((tokens + 3) / 4)), block, 0, stream, z,
-                       tokens, vocab, stride, labels, offsets, 2 * pairs, st, slope, grad_loss, out, out_stride);
-  else if (large)
-    hipLaunchKernelGGL((row_grad_kernel<TY, true, kThreads>), dim3(static_cast<unsigned>(tokens)), block, 0, stream, z, tokens,
-                       vocab, stride, labels, offsets, 2 * pairs, st, slope, grad_loss, out, out_stride);
-  else
-    hipLaunchKernelGGL((row_grad_kernel<TY, false, kThreads>), dim3(static_cast<unsigned>(tokens)), block, 0, stream, z, tokens,
-                       vocab, stride, labels, offsets, 2 * pairs, st, slope, grad_loss, out, out_stride);
+  const bool wide = vocab >= kWideGradRow || (tokens <= kFewTokens && vocab >= kLongRow);
+  const bool narrow = vocab <= kWaveRow && !large;
+  auto* kernel = narrow          ? row_grad_kernel<TY, false, 64>
+                 : large && wide ? row_grad_kernel<TY, true, 1024>
+                 : large         ? row_grad_kernel<TY, true, kThreads>
+                 : wide          ? row_grad_kernel<TY, false, 1024>
+                                 : row_grad_kernel<TY, false, kThreads>;
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(narrow ? (tokens + 3) / 4 : tokens)), dim3(wide ? 1024 : kThreads), 0,
+                     stream, z, tokens, vocab, stride, labels, offsets, 2 * pairs, st, slope, grad_loss, out, out_stride);
   return hipGetLastError();
 }
 
