@@ -132,14 +132,15 @@ Plan plan_of(bool across, int64_t m, int64_t n, int64_t k, int type, const void*
   // most CUs none:
   //   360 x 6362 x 660    dx 35 / 46             (tiled 30 / 37; 25 slices)
   //   4096 x 512 x 512    dW 20 / 28             (tiled 22 / 28; 16 slices)
+  //   1805 x 4824 x 474   dW 43 / 62             (tiled 33 / 52; 29 slices)
   // A gradient in parts costs the tiled form a pass over the codes for each,
   // and this one more where dy has to be transposed (dW).
   p.tiles64 = ((p.rows + 63) / 64) * ((p.cols + 63) / 64);
   p.ways = 1;
   while (p.ways < 8 && p.tiles64 * p.ways * 2 <= 2048 && p.stages > p.ways) p.ways *= 2;
-  const double most = p.parts == 1 ? 5e9 : p.parts == 2 ? 8e9 : 12e9;
+  const double most = p.parts == 1 ? 5e9 : p.parts == 2 ? 8e9 : 9e9;
   p.small = n >= 8 && static_cast<double>(p.depth) * p.rows * p.cols <= most &&
-            (p.tiles64 * p.ways >= 1024 || p.stages <= p.ways * (across ? 16 / p.parts : 16));
+            p.stages <= p.ways * (p.tiles64 * p.ways >= 1024 ? (across ? 20 : 32) : across ? 16 / p.parts : 16);
   if (p.small) {
     p.c_bytes = p.x_bytes = p.s_bytes = 0;
     return p;

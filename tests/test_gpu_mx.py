@@ -177,7 +177,8 @@ def test_gradients(m, n, k):
         assert torch.equal(got, B.mx8_grad_weight(strided(dy, 5, 3), x, out_dtype=T[out]))
 
 
-@pytest.mark.parametrize("m,n,k", [(70, 3900, 4200), (3900, 65, 4200), (3900, 4200, 90), (1000, 1003, 1500), (4096, 40, 3900), (1700, 1801, 1900), (4100, 4100, 300), (300, 6000, 100), (6000, 100, 300)])
+@pytest.mark.parametrize("m,n,k", [(70, 3900, 4200), (3900, 65, 4200), (3900, 4200, 90), (1000, 1003, 1500), (4096, 40, 3900), (1700, 1801, 1900), (4100, 4100, 300), (300, 6000, 100), (6000, 100, 300),
+                                   (3900, 600, 4200), (603, 3904, 4200)])
 def test_gradients_of_many_tiles(m, n, k):
     w, x = stored(values((n, k), 4), "mx4"), stored(values((m, k), 5), "mx8")
     wv = H.dequantize(w.codes.cpu().numpy(), w.scales.cpu().numpy(), k, "mx4")
